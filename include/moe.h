@@ -73,6 +73,7 @@ typedef enum {
 #define MOE_MAX_EXPERTS 256
 #define MOE_MAX_TOPK 8
 #define MOE_MAX_SHARED 8
+#define MOE_MAX_DECODE_TOKENS 64
 
 /* Stage boundaries at which optional timing events are recorded (see
  * moe_launch_t.stage_events): before the router, then after the router, the
@@ -292,6 +293,85 @@ moe_status_t moe_forward_noalloc(const void* x, const void* W_g, const void* W1,
                                  float capacity_factor, int32_t n_shared, void* out,
                                  int32_t* topk_idx, float* topk_w, float* aux_loss,
                                  const moe_launch_t* launch);
+
+/* ---- The layer for a few tokens ----------------------------------------------
+ * One generation step of a served model: moe_forward's layer for T in
+ * 1..MOE_MAX_DECODE_TOKENS tokens, without a capacity limit and without the
+ * training losses.  A call this small is bound by reading the taken experts'
+ * weights once, which moe_forward's 128- to 256-row tiles do at a fraction of
+ * the memory's rate; here waves stream the weights straight into matrix-core
+ * operands.  Arguments, layouts and selection rule as for moe_forward (logits
+ * in float64, ties to the lower expert index, a NaN logit below every number);
+ * the weights are normalised over the k chosen logits.  bf16 layers keep the
+ * hidden rows to 16 bits of mantissa and round the output once; float32 layers
+ * work in float32 throughout.  Two calls on the same inputs give the same bits.
+ * An expert's weights are read only if a token takes it, and they reach only
+ * the tokens that take it.
+ *
+ *   launch  T, d, h, dtype, b_g, b_sel, workspace, workspace_bytes, stream,
+ *           activation and weights_packed apply (the packed layout for bf16 and
+ *           d and h multiples of 256); expert_counts, expert_kept, slot_pos,
+ *           z_loss and stage_events must be NULL and min_capacity 0
+ *           (else MOE_ERR_UNSUPPORTED).  The stream must belong to the calling
+ *           thread's current device.  Calls that may overlap, graph replays among
+ *           them, need distinct workspaces; the contents need not be initialised.
+ * MOE_ERR_UNSUPPORTED also for T > MOE_MAX_DECODE_TOKENS, d or h above 2^20, and
+ * T (k + S) h above 2^28; other errors as for moe_forward. */
+size_t moe_workspace_bytes_decode(int32_t T, int32_t d, int32_t h, int32_t E, int32_t k, int32_t n_shared,
+                                  moe_dtype_t dtype);
+moe_status_t moe_forward_decode(const void* x, const void* W_g, const void* W1, const void* b1, const void* W2,
+                                const void* b2, int32_t E, int32_t k, int32_t n_shared, void* out,
+                                int32_t* topk_idx, float* topk_w, const moe_launch_t* launch);
+
+/* ---- 4-bit weights with group scales -------------------------------------------
+ *   w[n, j] = s[n, g] (q[n, j] - z[n, g]),  g = j / group,  group 32, 64 or 128
+ *   codes   uint8 [rows, cols/2]: q in 0..15, element 2i in the low nibble of byte
+ *           i of its row, element 2i + 1 in the high nibble; 16-byte aligned
+ *   scales  bf16 [rows, cols/group]; 2-byte aligned
+ *   zeros   uint8 [rows, cols/group] (the low four bits are read), or NULL: 8
+ * cols is the contracted dimension, a multiple of group.
+ *
+ * moe_quantize_w4: bf16 [rows, cols] (src 16-byte aligned) -> the above, per group
+ *   zeros NULL: s = bf16(max|v| / 7), q = round(v / s) + 8, clamped to 0..15
+ *   else: lo = min(v, 0), hi = max(v, 0) over the group, s = bf16((hi - lo) / 15),
+ *         z = round(-lo / s) clamped to 0..15, q = round(v / s) + z, clamped
+ * (ties to even; v / s in float32, (hi - lo) / 15 in float64).  A group whose s is
+ * zero gets q = z (z = 0 with zero points); one that holds an infinity or NaN gets
+ * s = NaN.
+ *
+ * moe_dequantize_w4: back to bf16 [rows, cols] (dst 16-byte aligned), each value
+ * rounded once: for long prompts through moe_forward.
+ *
+ * moe_linear_w4: y[m, n] = sum_j x[m, j] w[n, j] + bias[n] for M rows of bf16 x
+ * [M, K] (16-byte aligned), y [M, N] and bias [N] (or NULL) bf16; the sums in
+ * float32 on the unrounded s (q - z), y rounded once.  Made for a few rows: the
+ * codes are read once per 64 rows.  K at most 2^20, M at most 2^21 (else
+ * MOE_ERR_UNSUPPORTED).  An infinite x gives NaN in its row.
+ *
+ * Each enqueues on `stream` and returns MOE_OK, or MOE_ERR_ARG (a NULL required
+ * pointer, a size below 1), MOE_ERR_UNSUPPORTED (another group, cols or K not a
+ * multiple of it, alignment) or MOE_ERR_HIP. */
+moe_status_t moe_quantize_w4(const void* src, int32_t rows, int32_t cols, int32_t group, uint8_t* codes,
+                             void* scales, uint8_t* zeros, hipStream_t stream);
+moe_status_t moe_dequantize_w4(const uint8_t* codes, const void* scales, const uint8_t* zeros, int32_t rows,
+                               int32_t cols, int32_t group, void* dst, hipStream_t stream);
+moe_status_t moe_linear_w4(const void* x, int32_t M, const uint8_t* codes, const void* scales,
+                           const uint8_t* zeros, int32_t N, int32_t K, int32_t group, const void* bias, void* y,
+                           hipStream_t stream);
+
+/* moe_forward_decode on 4-bit expert weights (bf16 activations; the router and the
+ * biases stay bf16):
+ *   W1 [E+S, h, d/2] codes, W1_scales and W1_zeros [E+S, h, d/group]  (along d)
+ *   W2 [E+S, d, h/2] codes, W2_scales and W2_zeros [E+S, d, h/group]  (along h)
+ *   the zeros may be NULL, both or either; other arguments and launch fields as for
+ *   moe_forward_decode; launch->dtype must be MOE_BF16, weights_packed 0, d and h
+ *   multiples of group (else MOE_ERR_UNSUPPORTED). */
+size_t moe_workspace_bytes_decode_w4(int32_t T, int32_t d, int32_t h, int32_t E, int32_t k, int32_t n_shared);
+moe_status_t moe_forward_decode_w4(const void* x, const void* W_g, const uint8_t* W1, const void* W1_scales,
+                                   const uint8_t* W1_zeros, const void* b1, const uint8_t* W2,
+                                   const void* W2_scales, const uint8_t* W2_zeros, const void* b2, int32_t group,
+                                   int32_t E, int32_t k, int32_t n_shared, void* out, int32_t* topk_idx,
+                                   float* topk_w, const moe_launch_t* launch);
 
 /* Static, human-readable name of a status code. */
 const char* moe_status_string(moe_status_t s);

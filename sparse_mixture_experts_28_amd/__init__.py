@@ -17,7 +17,9 @@ from ._lib import (EXPORTS, LIB_PATH, MOE_ACT_GELU, MOE_ACT_SILU, MOE_BF16, MOE_
                    MOE_MAX_TOPK, MOE_NOALLOC_SCRATCH_BYTES, MOE_NUM_STAGE_EVENTS, MOE_OK, MoeLaunch,
                    moe_expert_choice_capacity, moe_forward, moe_forward_expert_choice, moe_forward_noalloc,
                    moe_forward_mxfp8, moe_pack_weights, moe_quantize_mxfp8, moe_status_string, moe_workspace_bytes,
-                   moe_workspace_bytes_expert_choice, moe_workspace_bytes_mxfp8)
+                   moe_workspace_bytes_expert_choice, moe_workspace_bytes_mxfp8, MOE_MAX_DECODE_TOKENS,
+                   moe_dequantize_w4, moe_forward_decode, moe_forward_decode_w4, moe_linear_w4, moe_quantize_w4,
+                   moe_workspace_bytes_decode, moe_workspace_bytes_decode_w4)
 
 ACTIVATIONS = {"gelu": MOE_ACT_GELU, "silu": MOE_ACT_SILU}
 
@@ -302,7 +304,203 @@ def forward_mxfp8(x, W_g, W1, W1s, b1, W2, W2s, b2, k: int, capacity_factor: flo
     return MoEOutput(out, topk_idx, topk_w, aux, zl, counts, kept, slot_pos)
 
 
-__all__ = ["forward", "MoEOutput", "moe_forward", "moe_workspace_bytes", "moe_status_string", "MoeLaunch",
+# ------------------------------------------------------ few-token operators --
+
+@dataclass
+class DecodeOutput:
+    out: "object"            # [T, d], dtype of x
+    topk_idx: "object"       # [T, k] int32
+    topk_w: "object"         # [T, k] float32
+
+
+def _on_device(dev):
+    """The device as the current one for the launches of a call (they go to its current stream)."""
+    import contextlib
+    import torch
+    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _decode_outputs(x, k, nbytes, workspace):
+    """Outputs and workspace of a few-token call; a workspace that is given has to be large enough."""
+    import torch
+    T, d = x.shape
+    if nbytes == 0:
+        raise RuntimeError("unsupported problem shape for the few-token layer")
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
+    elif workspace.device != x.device or not workspace.is_contiguous() or \
+            workspace.numel() * workspace.element_size() < nbytes:
+        raise ValueError(f"workspace must be a contiguous tensor of at least {nbytes} bytes on the same GPU")
+    return (torch.empty((T, d), dtype=x.dtype, device=x.device),
+            torch.empty((T, k), dtype=torch.int32, device=x.device),
+            torch.empty((T, k), dtype=torch.float32, device=x.device), workspace)
+
+
+def _decode_launch(x, h, dt, b_g, b_sel, activation, workspace):
+    import torch
+    launch = MoeLaunch()
+    launch.T, launch.d = x.shape
+    launch.h, launch.dtype = h, dt
+    launch.b_g = b_g.data_ptr() if b_g is not None else None
+    launch.b_sel = b_sel.data_ptr() if b_sel is not None else None
+    launch.workspace = workspace.data_ptr()
+    launch.workspace_bytes = workspace.numel() * workspace.element_size()
+    launch.stream = torch.cuda.current_stream(x.device).cuda_stream
+    launch.activation = ACTIVATIONS[activation]
+    return launch
+
+
+def _ptr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def forward_decode(x, W_g, W1, b1, W2, b2, k: int, n_shared: int = 0, b_g=None, *, activation: str = "gelu",
+                   b_sel=None, weights_packed: bool = False, workspace=None) -> DecodeOutput:
+    """``forward`` for 1..MOE_MAX_DECODE_TOKENS tokens (one generation step):
+    the same layer without a capacity limit and without the losses, made for
+    reading the taken experts' weights once.
+
+    Tensors as for ``forward``.  ``workspace``: a uint8 tensor of at least
+    ``moe_workspace_bytes_decode(T, d, h, E, k, n_shared, dtype)`` bytes, or
+    None (allocated).  Calls that may overlap, graph replays among them, need
+    workspaces of their own."""
+    _check_tensors(x, W_g, W1, b1, W2, b2, b_g, n_shared, activation)
+    E, h = W_g.shape[0], W1.shape[1]
+    _check_b_sel(b_sel, E, x.device)
+    dt = _dtype_code(x)
+    nbytes = moe_workspace_bytes_decode(x.shape[0], x.shape[1], h, E, k, n_shared, dt)
+    out, topk_idx, topk_w, workspace = _decode_outputs(x, k, nbytes, workspace)
+    launch = _decode_launch(x, h, dt, b_g, b_sel, activation, workspace)
+    launch.weights_packed = 1 if weights_packed else 0
+    with _on_device(x.device):
+        status = moe_forward_decode(x.data_ptr(), W_g.data_ptr(), W1.data_ptr(), _ptr(b1), W2.data_ptr(), _ptr(b2), E,
+                                    k, n_shared, out.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(), launch)
+    if status != MOE_OK:
+        raise RuntimeError(moe_status_string(status))
+    return DecodeOutput(out, topk_idx, topk_w)
+
+
+def _w4_group(codes, scales, zeros, dev) -> int:
+    """Checks one 4-bit tensor (codes [..., K/2], scales and zeros [..., K/group]); returns the group."""
+    import torch
+    for t, dt in ((codes, torch.uint8), (scales, torch.bfloat16), (zeros, torch.uint8)):
+        if t is not None and (not t.is_cuda or t.device != dev or not t.is_contiguous() or t.dtype != dt):
+            raise ValueError("4-bit weights are contiguous uint8 codes, bfloat16 scales and uint8 zeros on one GPU")
+    K, ng = 2 * codes.shape[-1], scales.shape[-1]
+    if scales.shape[:-1] != codes.shape[:-1] or (zeros is not None and zeros.shape != scales.shape) or ng < 1 or K % ng:
+        raise ValueError("inconsistent shapes of 4-bit codes, scales and zeros")
+    group = K // ng
+    if group not in (32, 64, 128):
+        raise ValueError("4-bit groups are 32, 64 or 128 elements")
+    return group
+
+
+def quantize_w4(w, group: int = 128, zero_points: bool = False):
+    """4-bit form of a bf16 tensor on the GPU along its last dimension K (a
+    multiple of ``group``: 32, 64 or 128): (codes uint8 [..., K/2], scales
+    bfloat16 [..., K/group], zeros uint8 [..., K/group], or None for the
+    symmetric form).  The rule is ``moe_quantize_w4``'s."""
+    import torch
+    if w.dtype != torch.bfloat16 or not w.is_cuda or not w.is_contiguous() or w.dim() < 1 or w.numel() == 0:
+        raise ValueError("quantize_w4 takes a contiguous, non-empty bf16 tensor on a GPU")
+    K = w.shape[-1]
+    if group not in (32, 64, 128) or K % group:
+        raise ValueError("group must be 32, 64 or 128 and divide the last dimension")
+    codes = torch.empty((*w.shape[:-1], K // 2), dtype=torch.uint8, device=w.device)
+    scales = torch.empty((*w.shape[:-1], K // group), dtype=torch.bfloat16, device=w.device)
+    zeros = torch.empty(scales.shape, dtype=torch.uint8, device=w.device) if zero_points else None
+    with _on_device(w.device):
+        st = moe_quantize_w4(w.data_ptr(), w.numel() // K, K, group, codes.data_ptr(), scales.data_ptr(), _ptr(zeros),
+                             torch.cuda.current_stream(w.device).cuda_stream)
+    if st != MOE_OK:
+        raise RuntimeError(moe_status_string(st))
+    return codes, scales, zeros
+
+
+def dequantize_w4(codes, scales, zeros=None):
+    """The bf16 tensor [..., K] that 4-bit codes [..., K/2], scales and zeros
+    [..., K/group] stand for (each value rounded once)."""
+    import torch
+    if codes.dim() < 1 or codes.numel() == 0:
+        raise ValueError("dequantize_w4 takes non-empty codes")
+    group = _w4_group(codes, scales, zeros, codes.device)
+    K = 2 * codes.shape[-1]
+    out = torch.empty((*codes.shape[:-1], K), dtype=torch.bfloat16, device=codes.device)
+    with _on_device(codes.device):
+        st = moe_dequantize_w4(codes.data_ptr(), scales.data_ptr(), _ptr(zeros), out.numel() // K, K, group,
+                               out.data_ptr(), torch.cuda.current_stream(codes.device).cuda_stream)
+    if st != MOE_OK:
+        raise RuntimeError(moe_status_string(st))
+    return out
+
+
+def linear_w4(x, codes, scales, zeros=None, bias=None):
+    """x [M, K] bf16 times a 4-bit weight (codes [N, K/2], scales and zeros
+    [N, K/group]) transposed, plus bias [N] bf16 or None: [M, N] bf16.  Made
+    for a few rows (the codes are read once per 64)."""
+    import torch
+    dev = x.device
+    if x.dtype != torch.bfloat16 or not x.is_cuda or not x.is_contiguous() or x.dim() != 2 or x.numel() == 0:
+        raise ValueError("linear_w4 takes a contiguous, non-empty bf16 [M, K] tensor on a GPU")
+    group = _w4_group(codes, scales, zeros, dev)
+    M, K = x.shape
+    N = codes.shape[0]
+    if codes.dim() != 2 or 2 * codes.shape[1] != K or N < 1:
+        raise ValueError("inconsistent shapes of x and the 4-bit weight")
+    if bias is not None and (bias.dtype != torch.bfloat16 or bias.shape != (N,) or bias.device != dev
+                             or not bias.is_contiguous()):
+        raise ValueError("bias must be a contiguous bf16 [N] on the same GPU")
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    with _on_device(dev):
+        st = moe_linear_w4(x.data_ptr(), M, codes.data_ptr(), scales.data_ptr(), _ptr(zeros), N, K, group, _ptr(bias),
+                           y.data_ptr(), torch.cuda.current_stream(dev).cuda_stream)
+    if st != MOE_OK:
+        raise RuntimeError(moe_status_string(st))
+    return y
+
+
+def forward_decode_w4(x, W_g, W1, W1s, W1z, b1, W2, W2s, W2z, b2, k: int, n_shared: int = 0, b_g=None, *,
+                      activation: str = "gelu", b_sel=None, workspace=None) -> DecodeOutput:
+    """``forward_decode`` on 4-bit expert weights: (codes, scales, zeros or None)
+    from ``quantize_w4`` of [E+S, h, d] and [E+S, d, h], one group size for
+    both; x, W_g and the biases bf16.  ``workspace``: at least
+    ``moe_workspace_bytes_decode_w4(T, d, h, E, k, n_shared)`` bytes, or None."""
+    import torch
+    dev = x.device
+    for t in (x, W_g, b1, b2):
+        if t is not None and (t.dtype != torch.bfloat16 or not t.is_cuda or t.device != dev or not t.is_contiguous()):
+            raise ValueError("x, W_g, b1 and b2 of the 4-bit layer must be contiguous bf16 tensors on one GPU")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    group = _w4_group(W1, W1s, W1z, dev)
+    if _w4_group(W2, W2s, W2z, dev) != group:
+        raise ValueError("W1 and W2 must have one group size")
+    T, d = x.shape
+    E, h, S = W_g.shape[0], W1.shape[1], n_shared
+    if W_g.shape != (E, d) or W1.shape != (E + S, h, d // 2) or W2.shape != (E + S, d, h // 2) or \
+            d % group or h % group or \
+            (b1 is not None and b1.shape != (E + S, h)) or (b2 is not None and b2.shape != (E + S, d)):
+        raise ValueError("inconsistent shapes")
+    if b_g is not None and (b_g.dtype != torch.float32 or b_g.shape != (E,) or b_g.device != dev
+                            or not b_g.is_contiguous()):
+        raise ValueError("b_g must be a contiguous float32 [E] on the same GPU")
+    _check_b_sel(b_sel, E, dev)
+    nbytes = moe_workspace_bytes_decode_w4(T, d, h, E, k, S)
+    out, topk_idx, topk_w, workspace = _decode_outputs(x, k, nbytes, workspace)
+    launch = _decode_launch(x, h, MOE_BF16, b_g, b_sel, activation, workspace)
+    with _on_device(dev):
+        status = moe_forward_decode_w4(x.data_ptr(), W_g.data_ptr(), W1.data_ptr(), W1s.data_ptr(), _ptr(W1z),
+                                       _ptr(b1), W2.data_ptr(), W2s.data_ptr(), _ptr(W2z), _ptr(b2), group, E, k, S,
+                                       out.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(), launch)
+    if status != MOE_OK:
+        raise RuntimeError(moe_status_string(status))
+    return DecodeOutput(out, topk_idx, topk_w)
+
+
+__all__ = ["forward_decode", "forward_decode_w4", "DecodeOutput", "quantize_w4", "dequantize_w4", "linear_w4",
+           "moe_forward_decode", "moe_forward_decode_w4", "moe_workspace_bytes_decode", "moe_workspace_bytes_decode_w4",
+           "moe_quantize_w4", "moe_dequantize_w4", "moe_linear_w4", "MOE_MAX_DECODE_TOKENS",
+           "forward", "MoEOutput", "moe_forward", "moe_workspace_bytes", "moe_status_string", "MoeLaunch",
            "forward_expert_choice", "ExpertChoiceOutput", "moe_forward_expert_choice",
            "moe_workspace_bytes_expert_choice", "expert_choice_capacity", "moe_expert_choice_capacity", "STAGES_EXPERT_CHOICE",
            "pack_weights", "moe_pack_weights", "quantize_mxfp8", "forward_mxfp8", "moe_quantize_mxfp8", "moe_workspace_bytes_mxfp8", "moe_forward_mxfp8",

@@ -31,12 +31,15 @@ MOE_NOALLOC_SCRATCH_BYTES = 64 << 20
 MOE_MAX_EXPERTS = 256
 MOE_MAX_TOPK = 8
 MOE_MAX_SHARED = 8
+MOE_MAX_DECODE_TOKENS = 64
 MOE_NUM_STAGE_EVENTS = 7
 
 # names of the C ABI entry points (include/moe.h)
 EXPORTS = ("moe_forward", "moe_workspace_bytes", "moe_status_string", "moe_forward_expert_choice",
            "moe_workspace_bytes_expert_choice", "moe_quantize_mxfp8", "moe_workspace_bytes_mxfp8",
-           "moe_forward_mxfp8", "moe_expert_choice_capacity", "moe_forward_noalloc", "moe_pack_weights")
+           "moe_forward_mxfp8", "moe_expert_choice_capacity", "moe_forward_noalloc", "moe_pack_weights",
+           "moe_workspace_bytes_decode", "moe_forward_decode", "moe_workspace_bytes_decode_w4",
+           "moe_forward_decode_w4", "moe_quantize_w4", "moe_dequantize_w4", "moe_linear_w4")
 
 
 class MoeLaunch(ctypes.Structure):
@@ -100,6 +103,21 @@ def _load():
                                      ctypes.c_void_p, ctypes.c_void_p]
     lib.moe_expert_choice_capacity.restype = ctypes.c_int32
     lib.moe_expert_choice_capacity.argtypes = [ctypes.c_float, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]
+    i32, ptr = ctypes.c_int32, ctypes.c_void_p
+    lib.moe_workspace_bytes_decode.restype = ctypes.c_size_t
+    lib.moe_workspace_bytes_decode.argtypes = [i32] * 6 + [ctypes.c_int]
+    lib.moe_forward_decode.restype = ctypes.c_int
+    lib.moe_forward_decode.argtypes = [ptr] * 6 + [i32] * 3 + [ptr] * 3 + [ctypes.POINTER(MoeLaunch)]
+    lib.moe_workspace_bytes_decode_w4.restype = ctypes.c_size_t
+    lib.moe_workspace_bytes_decode_w4.argtypes = [i32] * 6
+    lib.moe_forward_decode_w4.restype = ctypes.c_int
+    lib.moe_forward_decode_w4.argtypes = [ptr] * 10 + [i32] * 4 + [ptr] * 3 + [ctypes.POINTER(MoeLaunch)]
+    lib.moe_quantize_w4.restype = ctypes.c_int
+    lib.moe_quantize_w4.argtypes = [ptr, i32, i32, i32, ptr, ptr, ptr, ptr]
+    lib.moe_dequantize_w4.restype = ctypes.c_int
+    lib.moe_dequantize_w4.argtypes = [ptr, ptr, ptr, i32, i32, i32, ptr, ptr]
+    lib.moe_linear_w4.restype = ctypes.c_int
+    lib.moe_linear_w4.argtypes = [ptr, i32, ptr, ptr, ptr, i32, i32, i32, ptr, ptr, ptr]
     lib.moe_status_string.restype = ctypes.c_char_p
     lib.moe_status_string.argtypes = [ctypes.c_int]
     lib.moe_forward_noalloc.restype = ctypes.c_int
@@ -180,3 +198,39 @@ def moe_forward_mxfp8(x, W_g, W1, W1s, b1, W2, W2s, b2, E, k, capacity_factor, n
     """Raw call of the MXFP8 entry point: every array argument is a device address (int)."""
     return int(LIB.moe_forward_mxfp8(x, W_g, W1, W1s, b1, W2, W2s, b2, E, k, capacity_factor, n_shared, out,
                                      topk_idx, topk_w, aux_loss, ctypes.byref(launch)))
+
+
+def moe_workspace_bytes_decode(T: int, d: int, h: int, E: int, k: int, n_shared: int, dtype: int) -> int:
+    return int(LIB.moe_workspace_bytes_decode(T, d, h, E, k, n_shared, dtype))
+
+
+def moe_forward_decode(x, W_g, W1, b1, W2, b2, E, k, n_shared, out, topk_idx, topk_w, launch: MoeLaunch) -> int:
+    """Raw call of the few-token layer: every array argument is a device address (int)."""
+    return int(LIB.moe_forward_decode(x, W_g, W1, b1, W2, b2, E, k, n_shared, out, topk_idx, topk_w,
+                                      ctypes.byref(launch)))
+
+
+def moe_workspace_bytes_decode_w4(T: int, d: int, h: int, E: int, k: int, n_shared: int) -> int:
+    return int(LIB.moe_workspace_bytes_decode_w4(T, d, h, E, k, n_shared))
+
+
+def moe_forward_decode_w4(x, W_g, W1, W1s, W1z, b1, W2, W2s, W2z, b2, group, E, k, n_shared, out, topk_idx, topk_w,
+                          launch: MoeLaunch) -> int:
+    """Raw call of the few-token layer on 4-bit expert weights: every array argument is a device address (int)."""
+    return int(LIB.moe_forward_decode_w4(x, W_g, W1, W1s, W1z, b1, W2, W2s, W2z, b2, group, E, k, n_shared, out,
+                                         topk_idx, topk_w, ctypes.byref(launch)))
+
+
+def moe_quantize_w4(src, rows: int, cols: int, group: int, codes, scales, zeros, stream) -> int:
+    """Raw call: bf16 [rows, cols] at device address src -> 4-bit codes, scales and (or None) zero points."""
+    return int(LIB.moe_quantize_w4(src, rows, cols, group, codes, scales, zeros, stream))
+
+
+def moe_dequantize_w4(codes, scales, zeros, rows: int, cols: int, group: int, dst, stream) -> int:
+    """Raw call: 4-bit codes, scales and (or None) zero points -> bf16 [rows, cols] at dst."""
+    return int(LIB.moe_dequantize_w4(codes, scales, zeros, rows, cols, group, dst, stream))
+
+
+def moe_linear_w4(x, M: int, codes, scales, zeros, N: int, K: int, group: int, bias, y, stream) -> int:
+    """Raw call: y [M, N] = x [M, K] times the 4-bit [N, K] transposed, plus bias [N] or None."""
+    return int(LIB.moe_linear_w4(x, M, codes, scales, zeros, N, K, group, bias, y, stream))

@@ -295,6 +295,88 @@ moe_status_t forward_top_k(const void* x, const void* W_g, const void* W1, const
   return MOE_OK;
 }
 
+// ------------------------------------------------------ few-token operators --
+namespace {
+
+int group_shift(int32_t group) { return group == 32 ? 5 : group == 64 ? 6 : group == 128 ? 7 : -1; }
+
+// The few-row kernels address the activations, the hidden rows and 16 weight
+// rows through buffer ranges below 2^31 bytes.
+moe_status_t check_shape_decode(int32_t T, int32_t d, int32_t h, int32_t E, int32_t k, int32_t S, int dtype) {
+  const moe_status_t sc = check_shape(T, d, h, E, k, S, MOE_F32);   // the GEMM's bf16 ranges do not apply
+  if (sc != MOE_OK) return sc;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (T > MOE_MAX_DECODE_TOKENS || d > (1 << 20) || h > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+  if (static_cast<long long>(T) * (k + S) * h > (1LL << 28)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+struct DecodeLayout {
+  size_t logits, hid, part, counters, total;
+  int split, ncounter;
+};
+
+DecodeLayout decode_layout(int32_t T, int32_t d, int32_t h, int32_t E, int32_t k, int32_t S, int fmt) {
+  DecodeLayout L;
+  const long long row_bytes = fmt == kDecodeF32 ? 4LL * h : fmt == kDecodeBf16 ? 2LL * h : h / 2;
+  L.split = decode_split(T, d, h, E, k, S, row_bytes);
+  L.ncounter = (d + 15) / 16;
+  size_t off = 0;
+  L.logits = off;   off += align_up(static_cast<size_t>(T) * E * 8);
+  L.hid = off;      off += align_up(static_cast<size_t>(T) * (k + S) * h * 4);
+  L.part = off;     off += align_up(L.split > 1 ? static_cast<size_t>(L.split) * T * d * 4 : 0);
+  L.counters = off; off += align_up(static_cast<size_t>(L.ncounter) * 4);
+  L.total = off;
+  return L;
+}
+
+// Checks shared by moe_forward_decode and moe_forward_decode_w4, then the launch.
+// a: the weights, the format and the caller's other pointers.
+moe_status_t forward_decode(DecodeArgs a, const moe_launch_t* launch) {
+  if (launch->activation != MOE_ACT_GELU && launch->activation != MOE_ACT_SILU) return MOE_ERR_UNSUPPORTED;
+  if (launch->min_capacity < 0) return MOE_ERR_ARG;
+  if (launch->expert_counts || launch->expert_kept || launch->slot_pos || launch->z_loss || launch->stage_events ||
+      launch->min_capacity != 0)
+    return MOE_ERR_UNSUPPORTED;
+  const void* a16[] = {a.x, a.W_g, a.W1.w, a.b1, a.W2.w, a.b2, a.out};
+  for (const void* q : a16)
+    if (q && !aligned(q, 16)) return MOE_ERR_UNSUPPORTED;
+  const void* a4[] = {a.topk_idx, a.topk_w, launch->b_g, launch->b_sel};
+  for (const void* q : a4)
+    if (q && !aligned(q, 4)) return MOE_ERR_UNSUPPORTED;
+  a.b_g = launch->b_g;
+  a.b_sel = launch->b_sel;
+  a.T = launch->T;
+  a.d = launch->d;
+  a.h = launch->h;
+  a.act = launch->activation;
+  const DecodeLayout L = decode_layout(a.T, a.d, a.h, a.E, a.k, a.S, a.fmt);
+  if (launch->workspace == nullptr || launch->workspace_bytes < L.total || !aligned(launch->workspace, kAlign))
+    return MOE_ERR_WORKSPACE;
+  char* b = static_cast<char*>(launch->workspace);
+  a.logits = reinterpret_cast<double*>(b + L.logits);
+  a.hid = b + L.hid;
+  a.part = reinterpret_cast<float*>(b + L.part);
+  a.counters = reinterpret_cast<int32_t*>(b + L.counters);
+  a.ncounter = L.ncounter;
+  a.split = L.split;
+  (void)hipGetLastError();
+  const hipError_t e = launch_decode(a, launch->stream);
+  if (e != hipSuccess) {
+    std::fprintf(stderr, "libmoe: few-token layer launch failed: %s (%s)\n", hipGetErrorName(e), hipGetErrorString(e));
+    return MOE_ERR_HIP;
+  }
+  return MOE_OK;
+}
+
+moe_status_t w4_status(hipError_t e, const char* what) {
+  if (e == hipSuccess) return MOE_OK;
+  std::fprintf(stderr, "libmoe: %s launch failed: %s (%s)\n", what, hipGetErrorName(e), hipGetErrorString(e));
+  return MOE_ERR_HIP;
+}
+
+}  // namespace
+
 // ---------------------------------------------------- fixed device scratch --
 // The workspace of moe_forward_noalloc: one array per GPU, allocated when the
 // code object is loaded on that GPU and held until the process ends.  Host
@@ -446,6 +528,107 @@ moe_status_t moe_pack_weights(const void* W, int32_t n_mat, int32_t N, int32_t K
     return MOE_ERR_HIP;
   }
   return MOE_OK;
+}
+
+size_t moe_workspace_bytes_decode(int32_t T, int32_t d, int32_t h, int32_t E, int32_t k, int32_t n_shared,
+                                  moe_dtype_t dtype) {
+  if (moe::check_shape_decode(T, d, h, E, k, n_shared, static_cast<int>(dtype)) != MOE_OK) return 0;
+  return moe::decode_layout(T, d, h, E, k, n_shared, dtype == MOE_BF16 ? moe::kDecodeBf16 : moe::kDecodeF32).total;
+}
+
+size_t moe_workspace_bytes_decode_w4(int32_t T, int32_t d, int32_t h, int32_t E, int32_t k, int32_t n_shared) {
+  if (moe::check_shape_decode(T, d, h, E, k, n_shared, MOE_BF16) != MOE_OK) return 0;
+  if (d % 32 != 0 || h % 32 != 0) return 0;
+  return moe::decode_layout(T, d, h, E, k, n_shared, moe::kDecodeW4).total;
+}
+
+moe_status_t moe_forward_decode(const void* x, const void* W_g, const void* W1, const void* b1, const void* W2,
+                                const void* b2, int32_t E, int32_t k, int32_t n_shared, void* out,
+                                int32_t* topk_idx, float* topk_w, const moe_launch_t* launch) {
+  using namespace moe;
+  if (launch == nullptr) return MOE_ERR_ARG;
+  if (!x || !W_g || !W1 || !W2 || !out || !topk_idx || !topk_w) return MOE_ERR_ARG;
+  const moe_status_t sc = check_shape_decode(launch->T, launch->d, launch->h, E, k, n_shared,
+                                             static_cast<int>(launch->dtype));
+  if (sc != MOE_OK) return sc;
+  const int32_t d = launch->d, h = launch->h;
+  if (launch->weights_packed != 0 &&
+      (launch->weights_packed != 1 || launch->dtype != MOE_BF16 || d % 256 != 0 || h % 256 != 0))
+    return MOE_ERR_UNSUPPORTED;
+  DecodeArgs a{};
+  a.x = x; a.W_g = W_g; a.b1 = b1; a.b2 = b2; a.out = out; a.topk_idx = topk_idx; a.topk_w = topk_w;
+  a.E = E; a.k = k; a.S = n_shared;
+  a.fmt = launch->dtype == MOE_BF16 ? kDecodeBf16 : kDecodeF32;
+  a.W1 = WMat{static_cast<const char*>(W1), nullptr, nullptr, h, d, launch->weights_packed, 0};
+  a.W2 = WMat{static_cast<const char*>(W2), nullptr, nullptr, d, h, launch->weights_packed, 0};
+  return forward_decode(a, launch);
+}
+
+moe_status_t moe_forward_decode_w4(const void* x, const void* W_g, const uint8_t* W1, const void* W1_scales,
+                                   const uint8_t* W1_zeros, const void* b1, const uint8_t* W2,
+                                   const void* W2_scales, const uint8_t* W2_zeros, const void* b2, int32_t group,
+                                   int32_t E, int32_t k, int32_t n_shared, void* out, int32_t* topk_idx,
+                                   float* topk_w, const moe_launch_t* launch) {
+  using namespace moe;
+  if (launch == nullptr) return MOE_ERR_ARG;
+  if (!x || !W_g || !W1 || !W1_scales || !W2 || !W2_scales || !out || !topk_idx || !topk_w) return MOE_ERR_ARG;
+  const moe_status_t sc = check_shape_decode(launch->T, launch->d, launch->h, E, k, n_shared,
+                                             static_cast<int>(launch->dtype));
+  if (sc != MOE_OK) return sc;
+  const int32_t d = launch->d, h = launch->h;
+  const int gs = group_shift(group);
+  if (gs < 0 || d % group != 0 || h % group != 0 || launch->dtype != MOE_BF16 || launch->weights_packed != 0)
+    return MOE_ERR_UNSUPPORTED;
+  if (!aligned(W1_scales, 2) || !aligned(W2_scales, 2)) return MOE_ERR_UNSUPPORTED;
+  DecodeArgs a{};
+  a.x = x; a.W_g = W_g; a.b1 = b1; a.b2 = b2; a.out = out; a.topk_idx = topk_idx; a.topk_w = topk_w;
+  a.E = E; a.k = k; a.S = n_shared;
+  a.fmt = kDecodeW4;
+  a.W1 = WMat{reinterpret_cast<const char*>(W1), static_cast<const uint16_t*>(W1_scales), W1_zeros, h, d, 0, gs};
+  a.W2 = WMat{reinterpret_cast<const char*>(W2), static_cast<const uint16_t*>(W2_scales), W2_zeros, d, h, 0, gs};
+  return forward_decode(a, launch);
+}
+
+moe_status_t moe_quantize_w4(const void* src, int32_t rows, int32_t cols, int32_t group, uint8_t* codes,
+                             void* scales, uint8_t* zeros, hipStream_t stream) {
+  using namespace moe;
+  if (!src || !codes || !scales || rows < 1 || cols < 1) return MOE_ERR_ARG;
+  const int gs = group_shift(group);
+  if (gs < 0 || cols % group != 0) return MOE_ERR_UNSUPPORTED;
+  if (!aligned(src, 16) || !aligned(codes, 16) || !aligned(scales, 2)) return MOE_ERR_UNSUPPORTED;
+  (void)hipGetLastError();
+  return w4_status(launch_w4_quantize(static_cast<const uint16_t*>(src), static_cast<long long>(rows) * cols, gs, codes,
+                                      static_cast<uint16_t*>(scales), zeros, stream),
+                   "4-bit quantize");
+}
+
+moe_status_t moe_dequantize_w4(const uint8_t* codes, const void* scales, const uint8_t* zeros, int32_t rows,
+                               int32_t cols, int32_t group, void* dst, hipStream_t stream) {
+  using namespace moe;
+  if (!codes || !scales || !dst || rows < 1 || cols < 1) return MOE_ERR_ARG;
+  const int gs = group_shift(group);
+  if (gs < 0 || cols % group != 0) return MOE_ERR_UNSUPPORTED;
+  if (!aligned(dst, 16) || !aligned(codes, 16) || !aligned(scales, 2)) return MOE_ERR_UNSUPPORTED;
+  (void)hipGetLastError();
+  return w4_status(launch_w4_dequantize(codes, static_cast<const uint16_t*>(scales), zeros,
+                                        static_cast<long long>(rows) * cols, gs, static_cast<uint16_t*>(dst), stream),
+                   "4-bit dequantize");
+}
+
+moe_status_t moe_linear_w4(const void* x, int32_t M, const uint8_t* codes, const void* scales,
+                           const uint8_t* zeros, int32_t N, int32_t K, int32_t group, const void* bias, void* y,
+                           hipStream_t stream) {
+  using namespace moe;
+  if (!x || !codes || !scales || !y || M < 1 || N < 1 || K < 1) return MOE_ERR_ARG;
+  const int gs = group_shift(group);
+  if (gs < 0 || K % group != 0 || K > (1 << 20) || M > (1 << 21)) return MOE_ERR_UNSUPPORTED;
+  if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 2) || !aligned(y, 2) || (bias && !aligned(bias, 2)))
+    return MOE_ERR_UNSUPPORTED;
+  (void)hipGetLastError();
+  return w4_status(launch_w4_linear(static_cast<const uint16_t*>(x), M, codes, static_cast<const uint16_t*>(scales),
+                                    zeros, N, K, gs, static_cast<const uint16_t*>(bias), static_cast<uint16_t*>(y),
+                                    stream),
+                   "4-bit Linear");
 }
 
 const char* moe_status_string(moe_status_t s) {

@@ -319,6 +319,48 @@ constexpr int kGemmPartCap = 256;
 // the same in the fixed scratch of moe_forward_noalloc (16 tiles of 256 x 256 float32: 4 MB)
 constexpr int kNoallocPartTiles = 16;
 
+// ------------------------------------------------- few-token operators --
+// A weight matrix stack [n_mat][N][K] as the few-row kernels take it.
+struct WMat {
+  const char* w;
+  const uint16_t* s;   // 4-bit: scales
+  const uint8_t* z;    // 4-bit: zero points, or nullptr (8)
+  int N, K;
+  int packed;          // bf16: tile-packed layout
+  int gshift;          // 4-bit: log2 of the elements per scale
+};
+enum DecodeFmt { kDecodeF32 = 0, kDecodeBf16 = 1, kDecodeW4 = 2 };
+struct DecodeArgs {
+  const void* x;        // [T, d]
+  const void* W_g;      // [E, d]
+  const float* b_g;     // [E] or nullptr
+  const float* b_sel;   // [E] or nullptr
+  WMat W1, W2;          // [E+S][h][d], [E+S][d][h]
+  const void* b1;       // [E+S, h] or nullptr
+  const void* b2;       // [E+S, d] or nullptr
+  void* out;            // [T, d]
+  int32_t* topk_idx;    // [T, k]
+  float* topk_w;        // [T, k]
+  double* logits;       // [T, E]
+  void* hid;            // [T, k+S] hidden rows times the routing weight: h float32, or h bf16 values and h remainders
+  float* part;          // [split, T, d] float32 (split > 1)
+  int32_t* counters;    // ncounter, zeroed by the logits kernel
+  int ncounter;
+  int T, d, h, E, k, S;
+  int act;
+  int fmt;
+  int split;            // shares of phase 2's sum per 16 output columns
+};
+int decode_split(int T, int d, int h, int E, int k, int S, long long row_bytes);
+hipError_t launch_decode(const DecodeArgs& a, hipStream_t st);
+hipError_t launch_w4_quantize(const uint16_t* src, long long n, int gshift, uint8_t* codes, uint16_t* scales,
+                              uint8_t* zeros, hipStream_t st);
+hipError_t launch_w4_dequantize(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, long long n,
+                                int gshift, uint16_t* dst, hipStream_t st);
+hipError_t launch_w4_linear(const uint16_t* x, int M, const uint8_t* codes, const uint16_t* scales,
+                            const uint8_t* zeros, int N, int K, int gshift, const uint16_t* bias, uint16_t* y,
+                            hipStream_t st);
+
 // the top-k layer on a given workspace (moe_api.cpp)
 moe_status_t forward_top_k(const void* x, const void* W_g, const void* W1, const void* b1, const void* W2,
                            const void* b2, int32_t E, int32_t k, float capacity_factor, int32_t n_shared, void* out,

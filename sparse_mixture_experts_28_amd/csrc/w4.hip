@@ -1,0 +1,170 @@
+// 4-bit weights with group scales: the quantizer, its inverse and the Linear of a
+// few rows.
+//
+//   w[n, k] = s[n, g] (q[n, k] - z[n, g]),  g = k / group,  q in 0..15
+//
+// q two to a byte along k (even k in the low nibble), s bf16, z uint8 or 8.
+#include "few_rows.h"
+
+namespace moe {
+namespace {
+
+// ---------------------------------------------------------------- quantize --
+// A lane takes 8 consecutive elements, a group is group / 8 neighbouring lanes.
+// Quotients of bf16 numbers never fall within float32 rounding of a tie without
+// being one (both significands have 8 bits), so float32 division decides every
+// code as exact arithmetic does.
+__device__ __forceinline__ float group_max(float v, int lanes) {
+  for (int o = lanes >> 1; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+  return v;
+}
+
+template <bool ZERO>
+__global__ __launch_bounds__(256) void w4_quantize_kernel(const uint16_t* src, long long n8, int gshift,
+                                                          uint32_t* codes, uint16_t* scales, uint8_t* zeros) {
+  const int lanes = 1 << (gshift - 3);
+  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+  // n8 is a multiple of the lanes of a group, so a group is in or out as a whole
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n8; i += stride) {
+    const u32x4 raw = reinterpret_cast<const u32x4*>(src)[i];
+    float v[8];
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      v[2 * m] = __uint_as_float(raw[m] << 16);
+      v[2 * m + 1] = __uint_as_float(raw[m] & 0xffff0000u);
+    }
+    float hi = 0.f, lo = 0.f, bad = 0.f;   // lo: the largest -v
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+      bad = fabsf(v[m]) < INFINITY ? bad : 1.f;
+      hi = fmaxf(hi, v[m]);
+      lo = fmaxf(lo, -v[m]);
+    }
+    hi = group_max(hi, lanes);
+    lo = group_max(lo, lanes);
+    bad = group_max(bad, lanes);
+    uint16_t sb;
+    float z = 8.f;
+    if constexpr (ZERO) {
+      sb = f32_to_bf16(static_cast<float>((static_cast<double>(hi) + static_cast<double>(lo)) / 15.0));
+    } else {
+      sb = f32_to_bf16(fmaxf(hi, lo) / 7.f);
+    }
+    if (bad != 0.f) sb = 0x7fc0;   // a group with an infinity or NaN has no scale
+    const float s = bf16_to_f32(sb);
+    const bool fine = s > 0.f;      // false: all zero (or too small for a scale), or NaN
+    if constexpr (ZERO) z = fine ? fminf(rintf(lo / s), 15.f) : 0.f;
+    uint32_t c = 0;
+#pragma unroll
+    for (int m = 0; m < 8; ++m) {
+      const float q = fine ? fminf(fmaxf(rintf(v[m] / s) + z, 0.f), 15.f) : z;
+      c |= static_cast<uint32_t>(q) << (4 * m);
+    }
+    codes[i] = c;
+    if ((threadIdx.x & (lanes - 1)) == 0) {
+      const long long g = i >> (gshift - 3);
+      scales[g] = sb;
+      if constexpr (ZERO) zeros[g] = static_cast<uint8_t>(z);
+    }
+  }
+}
+
+// -------------------------------------------------------------- dequantize --
+// s (q - z): 8 bits times at most 5, exact in float32, one rounding to bf16.
+__global__ __launch_bounds__(256) void w4_dequantize_kernel(const uint32_t* codes, const uint16_t* scales,
+                                                            const uint8_t* zeros, long long n8, int gshift,
+                                                            uint16_t* dst) {
+  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
+  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n8; i += stride) {
+    const uint32_t c = codes[i];
+    const long long g = i >> (gshift - 3);
+    const float s = bf16_to_f32(scales[g]);
+    const int z = zeros != nullptr ? zeros[g] & 15 : 8;
+    u32x4 o;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const float a = s * static_cast<float>(static_cast<int>((c >> (8 * m)) & 15u) - z);
+      const float b = s * static_cast<float>(static_cast<int>((c >> (8 * m + 4)) & 15u) - z);
+      o[m] = static_cast<uint32_t>(f32_to_bf16(a)) | (static_cast<uint32_t>(f32_to_bf16(b)) << 16);
+    }
+    reinterpret_cast<u32x4*>(dst)[i] = o;
+  }
+}
+
+// ------------------------------------------------------------------ Linear --
+// y[m, n] = sum_k x[m, k] w[n, k] + b[n].  One workgroup per 16 columns and 64
+// rows; its waves split k and add their sums in LDS in wave order.
+template <int NT, int NW>
+__global__ __launch_bounds__(NW * 64) void w4_linear_kernel(const uint16_t* x, WMat w, const uint16_t* bias,
+                                                            uint16_t* y, int M) {
+  __shared__ float red[NT * NW * 256];
+  constexpr int U = 4;
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 64;
+  const int rows = min(M - m0, 64);
+  const uint32_t pitch = static_cast<uint32_t>(w.K) * 2u;
+  const __amdgpu_buffer_rsrc_t xr =
+      make_rsrc(x + static_cast<size_t>(m0) * w.K, static_cast<uint32_t>(rows) * pitch);
+  uint32_t aoff[NT];
+  floatx4 acc[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int p = j * 16 + (lane & 15);
+    aoff[j] = p < rows ? static_cast<uint32_t>(p) * pitch + 16u * (lane >> 4) : kOut;
+    acc[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+  }
+  const int tl = (rows + 15) / 16;
+  const int nst = (w.K + 127) / 128;
+  const int s0 = wave * nst / NW, s1 = (wave + 1) * nst / NW;
+  const WRows wr = rows_of<Fmt::kW4>(w, 0, n0, lane);
+  stream_rows<Fmt::kW4, NT, U>(acc, wr, xr, aoff, (1u << tl) - 1u, s0, s1, w.K, w.gshift, lane);
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+    *reinterpret_cast<floatx4*>(red + ((j * NW + wave) * 64 + lane) * 4) = acc[j];
+  __syncthreads();
+  for (int i = threadIdx.x; i < tl * 256; i += NW * 64) {
+    const int j = i >> 8, n = i & 15, pr = (i >> 4) & 15;
+    const int p = j * 16 + pr;
+    if (p >= rows || n0 + n >= w.N) continue;
+    const float* s = red + (j * NW * 64 + (pr >> 2) * 16 + n) * 4 + (pr & 3);
+    float v = 0.f;
+#pragma unroll
+    for (int q = 0; q < NW; ++q) v += s[q * 256];
+    if (bias != nullptr) v += bf16_to_f32(bias[n0 + n]);
+    y[static_cast<size_t>(m0 + p) * w.N + n0 + n] = f32_to_bf16(v);
+  }
+}
+
+int grid_of(long long n8) {
+  const long long g = (n8 + 255) / 256;
+  return static_cast<int>(g < 16384 ? g : 16384);
+}
+
+}  // namespace
+
+hipError_t launch_w4_quantize(const uint16_t* src, long long n, int gshift, uint8_t* codes, uint16_t* scales,
+                              uint8_t* zeros, hipStream_t st) {
+  uint32_t* c = reinterpret_cast<uint32_t*>(codes);
+  if (zeros != nullptr) w4_quantize_kernel<true><<<grid_of(n / 8), 256, 0, st>>>(src, n / 8, gshift, c, scales, zeros);
+  else w4_quantize_kernel<false><<<grid_of(n / 8), 256, 0, st>>>(src, n / 8, gshift, c, scales, zeros);
+  return hipGetLastError();
+}
+
+hipError_t launch_w4_dequantize(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, long long n,
+                                int gshift, uint16_t* dst, hipStream_t st) {
+  w4_dequantize_kernel<<<grid_of(n / 8), 256, 0, st>>>(reinterpret_cast<const uint32_t*>(codes), scales, zeros, n / 8,
+                                                      gshift, dst);
+  return hipGetLastError();
+}
+
+hipError_t launch_w4_linear(const uint16_t* x, int M, const uint8_t* codes, const uint16_t* scales,
+                            const uint8_t* zeros, int N, int K, int gshift, const uint16_t* bias, uint16_t* y,
+                            hipStream_t st) {
+  const WMat w{reinterpret_cast<const char*>(codes), scales, zeros, N, K, 0, gshift};
+  const dim3 grid((N + 15) / 16, (M + 63) / 64);
+  if (M <= 16) w4_linear_kernel<1, 8><<<grid, 512, 0, st>>>(x, w, bias, y, M);
+  else w4_linear_kernel<4, 8><<<grid, 512, 0, st>>>(x, w, bias, y, M);
+  return hipGetLastError();
+}
+
+}  // namespace moe

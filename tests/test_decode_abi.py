@@ -1,0 +1,125 @@
+"""The few-token entry points' checks of arguments, on the host before any GPU
+call (no call here reaches a kernel)."""
+import pytest
+
+import sparse_mixture_experts_28_amd as moe
+
+FAKE = 0x10000   # aligned, never dereferenced
+
+DEC = dict(x=FAKE, W_g=FAKE, W1=FAKE, b1=FAKE, W2=FAKE, b2=FAKE, E=8, k=2, S=0, out=FAKE, idx=FAKE, w=FAKE)
+W4 = dict(DEC, W1s=FAKE, W1z=FAKE, W2s=FAKE, W2z=FAKE, group=32)
+
+
+def decode(w4=False, **kw):
+    a = dict(W4 if w4 else DEC)
+    f = dict(T=4, d=64, h=96, dtype=moe.MOE_BF16, workspace=FAKE)
+    L = moe.MoeLaunch()
+    for key, v in kw.items():
+        if key in a:
+            a[key] = v
+        else:
+            f[key] = v
+    for key, v in f.items():
+        setattr(L, key, v)
+    if "workspace_bytes" not in f:
+        # one byte short of what is needed, so that an accepted call still stops before its launch
+        need = (moe.moe_workspace_bytes_decode_w4(L.T, L.d, L.h, a["E"], a["k"], a["S"]) if w4 else
+                moe.moe_workspace_bytes_decode(L.T, L.d, L.h, a["E"], a["k"], a["S"], L.dtype))
+        L.workspace_bytes = max(need, 1) - 1
+    if w4:
+        return moe.moe_forward_decode_w4(a["x"], a["W_g"], a["W1"], a["W1s"], a["W1z"], a["b1"], a["W2"], a["W2s"],
+                                         a["W2z"], a["b2"], a["group"], a["E"], a["k"], a["S"], a["out"], a["idx"],
+                                         a["w"], L)
+    return moe.moe_forward_decode(a["x"], a["W_g"], a["W1"], a["b1"], a["W2"], a["b2"], a["E"], a["k"], a["S"],
+                                  a["out"], a["idx"], a["w"], L)
+
+
+@pytest.mark.parametrize("w4", [False, True])
+def test_accepted_up_to_the_workspace(w4):
+    ok = moe.MOE_ERR_WORKSPACE   # everything before it was accepted
+    assert decode(w4) == ok
+    assert decode(w4, T=1) == ok and decode(w4, T=64) == ok
+    assert decode(w4, b1=None, b2=None, b_g=FAKE, b_sel=FAKE, activation=moe.MOE_ACT_SILU) == ok
+    assert decode(w4, E=256, k=8, S=8) == ok
+    assert decode(w4, d=1 << 20, h=128) == ok
+    assert decode(w4, workspace=None) == ok and decode(w4, workspace=FAKE + 16, workspace_bytes=1 << 30) == ok
+
+
+@pytest.mark.parametrize("w4", [False, True])
+def test_null_pointers(w4):
+    required = ["x", "W_g", "W1", "W2", "out", "idx", "w"] + (["W1s", "W2s"] if w4 else [])
+    for name in required:
+        assert decode(w4, **{name: None}) == moe.MOE_ERR_ARG, name
+    if w4:
+        assert decode(w4, W1z=None) == moe.MOE_ERR_WORKSPACE and decode(w4, W2z=None) == moe.MOE_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("w4", [False, True])
+def test_shapes(w4):
+    for kw in (dict(T=0), dict(T=-1), dict(d=0), dict(h=0), dict(E=0), dict(k=0), dict(k=9, E=8), dict(S=-1),
+               dict(min_capacity=-1)):
+        assert decode(w4, **kw) == moe.MOE_ERR_ARG, kw
+    for kw in (dict(T=65), dict(d=(1 << 20) + 128), dict(h=(1 << 20) + 128), dict(T=64, h=1 << 20, k=8),
+               dict(E=257), dict(k=9, E=16), dict(S=9), dict(dtype=7), dict(activation=2), dict(min_capacity=4),
+               dict(expert_counts=FAKE), dict(expert_kept=FAKE), dict(slot_pos=FAKE), dict(z_loss=FAKE),
+               dict(stage_events=FAKE), dict(weights_packed=2), dict(weights_packed=1)):
+        assert decode(w4, **kw) == moe.MOE_ERR_UNSUPPORTED, kw
+    if w4:
+        for kw in (dict(group=16), dict(group=256), dict(group=64), dict(d=72), dict(h=48), dict(dtype=moe.MOE_F32),
+                   dict(d=256, h=256, weights_packed=1)):
+            assert decode(w4, **kw) == moe.MOE_ERR_UNSUPPORTED, kw
+    else:
+        assert decode(d=68) == moe.MOE_ERR_UNSUPPORTED and decode(h=100) == moe.MOE_ERR_UNSUPPORTED
+        assert decode(d=256, h=256, weights_packed=1) == moe.MOE_ERR_WORKSPACE
+        assert decode(d=256, h=256, weights_packed=1, dtype=moe.MOE_F32) == moe.MOE_ERR_UNSUPPORTED
+        assert decode(d=72, h=104, dtype=moe.MOE_F32) == moe.MOE_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("w4", [False, True])
+def test_alignment(w4):
+    for name in ["x", "W_g", "W1", "b1", "W2", "b2", "out"]:
+        assert decode(w4, **{name: FAKE + 8}) == moe.MOE_ERR_UNSUPPORTED, name
+    for name in ["idx", "w", "b_g", "b_sel"]:
+        assert decode(w4, **{name: FAKE + 2}) == moe.MOE_ERR_UNSUPPORTED, name
+    if w4:
+        assert decode(True, W1s=FAKE + 1) == moe.MOE_ERR_UNSUPPORTED
+        assert decode(True, W2s=FAKE + 2, W1z=FAKE + 1) == moe.MOE_ERR_WORKSPACE
+
+
+def test_workspace_bytes():
+    f = moe.moe_workspace_bytes_decode
+    assert f(1, 4096, 14336, 8, 2, 0, moe.MOE_BF16) < 8 << 20
+    assert f(64, 7168, 2048, 256, 8, 1, moe.MOE_BF16) < 64 << 20
+    for bad in [(0, 64, 64, 8, 2, 0), (65, 64, 64, 8, 2, 0), (4, 60, 64, 8, 2, 0), (4, 64, 64, 8, 9, 0),
+                (4, 64, 64, 257, 2, 0)]:
+        assert f(*bad, moe.MOE_BF16) == 0, bad
+        assert moe.moe_workspace_bytes_decode_w4(*bad) == 0, bad
+    assert f(4, 64, 64, 8, 2, 0, 5) == 0 and moe.moe_workspace_bytes_decode_w4(4, 72, 64, 8, 2, 0) == 0
+
+
+def test_w4_calls():
+    q = lambda **k: moe.moe_quantize_w4(*[dict(dict(src=FAKE, rows=4, cols=128, group=64, codes=FAKE, scales=FAKE,
+                                                   zeros=None, stream=None), **k)[n]
+                                         for n in ("src", "rows", "cols", "group", "codes", "scales", "zeros", "stream")])
+    d = lambda **k: moe.moe_dequantize_w4(*[dict(dict(codes=FAKE, scales=FAKE, zeros=None, rows=4, cols=128, group=64,
+                                                     dst=FAKE, stream=None), **k)[n]
+                                           for n in ("codes", "scales", "zeros", "rows", "cols", "group", "dst", "stream")])
+    li = lambda **k: moe.moe_linear_w4(*[dict(dict(x=FAKE, M=4, codes=FAKE, scales=FAKE, zeros=None, N=32, K=128,
+                                                  group=64, bias=None, y=FAKE, stream=None), **k)[n]
+                                        for n in ("x", "M", "codes", "scales", "zeros", "N", "K", "group", "bias", "y",
+                                                  "stream")])
+    for call, null, size in ((q, ("src", "codes", "scales"), ("rows", "cols")),
+                             (d, ("codes", "scales", "dst"), ("rows", "cols")),
+                             (li, ("x", "codes", "scales", "y"), ("M", "N", "K"))):
+        for name in null:
+            assert call(**{name: None}) == moe.MOE_ERR_ARG, name
+        for name in size:
+            assert call(**{name: 0}) == moe.MOE_ERR_ARG and call(**{name: -4}) == moe.MOE_ERR_ARG, name
+        for g in (0, 16, 48, 256, -32):
+            assert call(group=g) == moe.MOE_ERR_UNSUPPORTED, g
+        assert call(codes=FAKE + 8) == moe.MOE_ERR_UNSUPPORTED and call(scales=FAKE + 1) == moe.MOE_ERR_UNSUPPORTED
+    assert q(cols=96) == moe.MOE_ERR_UNSUPPORTED and d(cols=96) == moe.MOE_ERR_UNSUPPORTED
+    assert li(K=96) == moe.MOE_ERR_UNSUPPORTED and li(K=(1 << 20) + 64) == moe.MOE_ERR_UNSUPPORTED
+    assert q(src=FAKE + 2) == moe.MOE_ERR_UNSUPPORTED and d(dst=FAKE + 2) == moe.MOE_ERR_UNSUPPORTED
+    assert li(x=FAKE + 8) == moe.MOE_ERR_UNSUPPORTED and li(bias=FAKE + 1) == moe.MOE_ERR_UNSUPPORTED
+    assert li(M=(1 << 21) + 1) == moe.MOE_ERR_UNSUPPORTED
