@@ -31,52 +31,52 @@ __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t voff,
                                                                          static_cast<int>(soff), 0));
 }
 
-// Weight formats.
-//   kK     k of one step (all four quarters)
-//   kLane  k of one lane's 16-byte load
-//   kActs  16-byte activation loads per lane and step
-enum class Fmt { kF32, kBf16, kW4 };
-template <Fmt F> struct FmtOf;
-template <> struct FmtOf<Fmt::kF32> { static constexpr int kK = 16, kLane = 4, kActs = 1; };
-template <> struct FmtOf<Fmt::kBf16> { static constexpr int kK = 32, kLane = 8, kActs = 1; };
-template <> struct FmtOf<Fmt::kW4> { static constexpr int kK = 128, kLane = 32, kActs = 4; };
+// Weight formats; 4-bit codes by their group.
+enum class Fmt { kF32, kBf16, kW4g32, kW4g64, kW4g128 };
+constexpr bool is_w4(Fmt f) { return f != Fmt::kF32 && f != Fmt::kBf16; }
+// k of one step (all four quarters), of one lane's 16-byte load, and of one MFMA
+constexpr int step_k(Fmt f) { return f == Fmt::kF32 ? 16 : f == Fmt::kBf16 ? 32 : 128; }
+constexpr int lane_k(Fmt f) { return step_k(f) / 4; }
+constexpr int group_shift(Fmt f) { return f == Fmt::kW4g32 ? 5 : f == Fmt::kW4g64 ? 6 : 7; }
+constexpr int acts(Fmt f) { return is_w4(f) ? 4 : 1; }   // 16-byte activation loads per lane and step
 
-// Where a wave finds 16 rows of W.  Step s's load is at voff[s & 1] + (s >> 1) *
-// pair: row-major matrices advance 128 bytes per two steps (voff[1] = voff[0] +
-// 64); in the tile-packed layout two steps are one 64-column block, 32 KB apart,
-// with the lane's chunk at a position of its own in either half.
-// 4-bit: scales [n, K/G] bf16 and zero points [n, K/G] uint8 (or none: 8).
+// Where a wave finds 16 RT rows of W.  Step s's load of row tile r is at
+// voff[s & 1] + r * tile + (s >> 1) * pair: row-major matrices advance 128 bytes
+// per two steps (voff[1] = voff[0] + 64); in the tile-packed layout two steps
+// are one 64-column block, 32 KB apart, with the lane's chunk at a position of
+// its own in either half.
+// 4-bit: scales [n, K/group] bf16 and zero points [n, K/group] uint8 (or none: 8).
 struct WRows {
   __amdgpu_buffer_rsrc_t w;
   uint32_t voff[2];
-  uint32_t pair;
-  __amdgpu_buffer_rsrc_t s, z;   // 4-bit: this tile's scale and zero-point rows
-  uint32_t srow;                 // 4-bit: first scale of the lane's row (elements)
-  bool has_z;
+  uint32_t pair, tile;
+  __amdgpu_buffer_rsrc_t s, z;   // 4-bit: the rows' scales and zero points
+  uint32_t srow, stile;          // 4-bit: first scale of the lane's row, scales of 16 rows
 };
 
-template <Fmt F>
+template <Fmt F, int RT>
 __device__ __forceinline__ WRows rows_of(const WMat& m, long long mat, int n0, int lane) {
   const int r = lane & 15, q = lane >> 4;
   WRows o;
-  const int left = min(16, m.N - n0);
-  if constexpr (F == Fmt::kW4) {
+  const int left = min(16 * RT, m.N - n0);
+  if constexpr (is_w4(F)) {
     const uint32_t pitch = static_cast<uint32_t>(m.K) / 2;
-    const uint32_t ng = static_cast<uint32_t>(m.K) >> m.gshift;
+    const uint32_t ng = static_cast<uint32_t>(m.K) >> group_shift(F);
     const long long row0 = mat * m.N + n0;
     o.w = make_rsrc(m.w + row0 * pitch, static_cast<uint32_t>(left) * pitch);
     o.voff[0] = static_cast<uint32_t>(r) * pitch + 16u * q;
     o.voff[1] = o.voff[0] + 64u;
     o.pair = 128u;
+    o.tile = 16u * pitch;
     o.s = make_rsrc(m.s + row0 * ng, static_cast<uint32_t>(left) * ng * 2u);
-    o.has_z = m.z != nullptr;
     o.z = o.s;
-    if (o.has_z) o.z = make_rsrc(m.z + row0 * ng, static_cast<uint32_t>(left) * ng);
+    if (m.z != nullptr) o.z = make_rsrc(m.z + row0 * ng, static_cast<uint32_t>(left) * ng);
     o.srow = static_cast<uint32_t>(r) * ng;
+    o.stile = 16u * ng;
   } else {
     constexpr uint32_t eb = F == Fmt::kF32 ? 4 : 2;
     const uint32_t pitch = static_cast<uint32_t>(m.K) * eb;
-    if (F == Fmt::kBf16 && m.packed) {
+    if (F == Fmt::kBf16 && m.packed) {   // 16 RT rows stay in one 256-row block
       const uint32_t nkb = static_cast<uint32_t>(m.K) / 64;
       const uint32_t r256 = static_cast<uint32_t>(n0 % 256 + r);
       const long long blk = (mat * (m.N / 256) + n0 / 256) * nkb;
@@ -85,148 +85,222 @@ __device__ __forceinline__ WRows rows_of(const WMat& m, long long mat, int n0, i
       o.voff[0] = r256 * 128u + ((static_cast<uint32_t>(q) ^ sw) * 16u);
       o.voff[1] = r256 * 128u + ((static_cast<uint32_t>(4 + q) ^ sw) * 16u);
       o.pair = 32768u;
+      o.tile = 2048u;
     } else {
       o.w = make_rsrc(m.w + (mat * m.N + n0) * pitch, static_cast<uint32_t>(left) * pitch);
       o.voff[0] = static_cast<uint32_t>(r) * pitch + 16u * q;
       o.voff[1] = o.voff[0] + 64u;
       o.pair = 128u;
+      o.tile = 16u * pitch;
     }
     o.s = o.z = o.w;
-    o.srow = 0;
-    o.has_z = false;
+    o.srow = o.stile = 0;
   }
   return o;
 }
 
 // ------------------------------------------------------------ 4-bit codes --
-// A lane's 16 bytes are 32 codes of one row; the four lane quarters hold 128
-// consecutive k.  A scale covers 32 k or a multiple, and an MFMA sums over the
-// quarters, so each MFMA must take its 32 k from one block of 32: the dwords
-// are exchanged between the quarters as a 4 x 4 transpose (dword g of quarter
-// q becomes dword q of quarter g), two register swaps per stage.
-__device__ __forceinline__ void transpose_quarters(u32x4& v) {
-  // halves: (q0 q1 | q2 q3) dwords 0,1 of the upper half against 2,3 of the lower
-  auto a = __builtin_amdgcn_permlane32_swap(v.x, v.z, false, false);
-  auto b = __builtin_amdgcn_permlane32_swap(v.y, v.w, false, false);
-  auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-  auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-  v.x = c[0];
-  v.y = c[1];
-  v.z = d[0];
-  v.w = d[1];
-}
-
 // Eight codes of a dword as bf16 numbers 128 + q: 0x4300 is 128 with a last
 // place of 1, so a code is its low bits.  Register i holds codes i and i + 4.
-__device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t w) {
+// (The constant comes in a register: an instruction reads one scalar at most,
+// and and-or takes the mask from it.)
+__device__ __forceinline__ uint32_t code_base() {
+  uint32_t v;
+  __asm__("v_mov_b32 %0, 0x43004300" : "=v"(v));
+  return v;
+}
+__device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t w, uint32_t base) {
   u32x4 o;
-  o.x = (w & 0x000f000fu) | 0x43004300u;
-  o.y = ((w >> 4) & 0x000f000fu) | 0x43004300u;
-  o.z = ((w >> 8) & 0x000f000fu) | 0x43004300u;
-  o.w = ((w >> 12) & 0x000f000fu) | 0x43004300u;
+  o.x = (w & 0x000f000fu) | base;
+  o.y = ((w >> 4) & 0x000f000fu) | base;
+  o.z = ((w >> 8) & 0x000f000fu) | base;
+  o.w = ((w >> 12) & 0x000f000fu) | base;
   return __builtin_bit_cast(bf16x8, o);
 }
 
-// Eight consecutive bf16 activations in the order of codes_to_bf16:
-// (0,4) (1,5) (2,6) (3,7).
-__device__ __forceinline__ bf16x8 acts_in_code_order(u32x4 v) {
+// Position of element k of a row in that order, within its block of eight:
+// 0 4 1 5 2 6 3 7.  Activations meant for 4-bit weights are stored so.
+__host__ __device__ constexpr int code_order(int k) {
+  return (k & ~7) | ((k & 7) < 4 ? 2 * (k & 7) : 2 * (k & 7) - 7);
+}
+// eight consecutive bf16 activations put into it
+__device__ __forceinline__ u32x4 to_code_order(u32x4 v) {
   u32x4 o;
   o.x = __builtin_amdgcn_perm(v.z, v.x, 0x05040100u);
   o.y = __builtin_amdgcn_perm(v.z, v.x, 0x07060302u);
   o.z = __builtin_amdgcn_perm(v.w, v.y, 0x05040100u);
   o.w = __builtin_amdgcn_perm(v.w, v.y, 0x07060302u);
-  return __builtin_bit_cast(bf16x8, o);
+  return o;
 }
 
-// value v of quarter g in all four quarters
-__device__ __forceinline__ void spread_quarters(uint32_t v, uint32_t (&o)[4]) {
-  auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);   // h[0]: q0 q1 q0 q1, h[1]: q2 q3 q2 q3
-  auto a = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
-  auto b = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
-  o[0] = a[0];
-  o[1] = a[1];
-  o[2] = b[0];
-  o[3] = b[1];
+// An MFMA sums over the lane quarters, so its k must lie in one group.  A
+// lane's four dwords are k q 32 + 8 i; within groups of 128 they may stay,
+// within groups of 64 the halves exchange dwords (0, 1 of the upper lanes
+// against 2, 3 of the lower), within groups of 32 the quarters too (a 4 x 4
+// transpose).  MFMA i then takes, in quarter q, the k from quarter_k(q) +
+// mfma_k(i) of the step on.
+template <Fmt F>
+__device__ __forceinline__ void arrange_codes(u32x4& v) {
+  if constexpr (F == Fmt::kW4g128) return;
+  auto a = __builtin_amdgcn_permlane32_swap(v.x, v.z, false, false);
+  auto b = __builtin_amdgcn_permlane32_swap(v.y, v.w, false, false);
+  if constexpr (F == Fmt::kW4g64) {
+    v.x = a[0];
+    v.y = b[0];
+    v.z = a[1];
+    v.w = b[1];
+  } else {
+    auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    v.x = c[0];
+    v.y = c[1];
+    v.z = d[0];
+    v.w = d[1];
+  }
+}
+template <Fmt F> __device__ __forceinline__ int quarter_k(int q) {
+  if constexpr (F == Fmt::kW4g128) return 32 * q;
+  else if constexpr (F == Fmt::kW4g64) return 32 * (q & 1) + 16 * (q >> 1);
+  else return lane_k(F) < 8 ? 4 * q : 8 * q;   // 4-bit groups of 32, bf16; float32
+}
+template <Fmt F> constexpr int mfma_k(int i) {
+  return F == Fmt::kW4g128 ? 8 * i : F == Fmt::kW4g64 ? 8 * (i & 1) + 64 * (i >> 1) : 32 * i;
+}
+
+// Scales of a step: a lane loads the one of its own 32 k; o[g]: that of the
+// step's group g in every lane of the row.
+template <Fmt F>
+__device__ __forceinline__ void spread_scales(uint32_t v, uint32_t (&o)[4]) {
+  o[0] = v;
+  if constexpr (F == Fmt::kW4g128) return;
+  auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  if constexpr (F == Fmt::kW4g64) {
+    o[0] = h[0];
+    o[1] = h[1];
+  } else {
+    auto a = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+    auto b = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+    o[0] = a[0];
+    o[1] = a[1];
+    o[2] = b[0];
+    o[3] = b[1];
+  }
 }
 
 // ------------------------------------------------------------- streaming --
-// acc[j] += A rows of tile j times the 16 rows of W over steps [s0, s1) (of a
-// matrix with K columns), for the tiles of `tiles` (bit j).  a: activations;
-// aoff[j] the lane's byte offset of row (lane % 16) of tile j plus 16 q, or
-// kOut for an empty row.  U steps are loaded together.
-template <Fmt F, int NT, int U>
-__device__ __forceinline__ void stream_rows(floatx4 (&acc)[NT], const WRows& wr, __amdgpu_buffer_rsrc_t a,
-                                            const uint32_t (&aoff)[NT], uint32_t tiles, int s0, int s1, int K,
-                                            int gshift, int lane) {
-  using Ff = FmtOf<F>;
-  static_assert(U % 2 == 0, "a batch starts at the parity of s0");
+// acc[j][r] += A rows of tile j times the 16 rows of W tile r over steps
+// [s0, s1) (of a matrix with K columns), for the first ntile tiles.
+// a: activations; aoff[j] the byte offset of the lane's row (lane % 16) of tile
+// j, or kOut for an empty row.  U steps are loaded together.
+// 4-bit: sum (q - z) x over a group is sum (128 + q) x - sum 136 x + (8 - z)
+// sum x.  The products are exact in float32; the middle sum depends on the
+// activations alone, is formed once for all RT tiles and starts the first; the
+// last takes it times -(8 - z) / 136.  kOrdered: the activations are stored in
+// code_order.
+template <Fmt F, int NT, int RT, int U, bool kOrdered, bool kZ>
+__device__ __forceinline__ void stream_rows(floatx4 (&acc)[NT][RT], const WRows& wr,
+                                            __amdgpu_buffer_rsrc_t a, const uint32_t (&arow)[NT], int ntile, int s0,
+                                            int s1, int K, int lane) {
+  constexpr int kK = step_k(F), kA = acts(F);
+  constexpr uint32_t kXe = F == Fmt::kF32 ? 4 : 2;   // bytes of an activation
   const int q = lane >> 4;
-  const int kend = min(K, s1 * Ff::kK);
-  const uint32_t v0 = s0 & 1 ? wr.voff[1] : wr.voff[0], v1 = s0 & 1 ? wr.voff[0] : wr.voff[1];
+  const int kend = min(K, s1 * kK);
+  const uint32_t xq = static_cast<uint32_t>(quarter_k<F>(q)) * kXe;
+  uint32_t base = 0;
+  u32x4 neg = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};   // -136
+  if constexpr (is_w4(F)) base = code_base();
   for (int sb = s0; sb < s1; sb += U) {
-    u32x4 w[U];
-    uint32_t sc[U];
+    u32x4 w[U][RT];
+    uint32_t sc[U][RT], zc[U][RT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int s = sb + u;
-      const bool in = s * Ff::kK + q * Ff::kLane < kend;
-      w[u] = load16(wr.w, in ? (u & 1 ? v1 : v0) : kOut, static_cast<uint32_t>(s >> 1) * wr.pair);
-      if constexpr (F == Fmt::kW4) {
-        // the lane's scale (high half) and its zero point as the bf16 number
-        // -(128 + z) (low half)
-        const uint32_t gi = wr.srow + (static_cast<uint32_t>(s * Ff::kK + q * Ff::kLane) >> gshift);
-        const uint32_t sv = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(
-            wr.s, static_cast<int>(in ? gi * 2u : kOut), 0, 0));
-        uint32_t zv = 8;
-        if (wr.has_z)
-          zv = static_cast<uint8_t>(__builtin_amdgcn_raw_buffer_load_b8(wr.z, static_cast<int>(in ? gi : kOut), 0, 0));
-        sc[u] = (sv << 16) | 0xc300u | (zv & 15u);
+      const bool in = s * kK + q * lane_k(F) < kend;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        w[u][r] = load16(wr.w, in ? (s & 1 ? wr.voff[1] : wr.voff[0]) + r * wr.tile : kOut,
+                         static_cast<uint32_t>(s >> 1) * wr.pair);
+        if constexpr (is_w4(F)) {
+          const uint32_t gi = wr.srow + r * wr.stile + (static_cast<uint32_t>(s * kK + q * 32) >> group_shift(F));
+          sc[u][r] = static_cast<uint16_t>(
+              __builtin_amdgcn_raw_buffer_load_b16(wr.s, static_cast<int>(in ? gi * 2u : kOut), 0, 0));
+          if constexpr (kZ)
+            zc[u][r] = static_cast<uint8_t>(
+                __builtin_amdgcn_raw_buffer_load_b8(wr.z, static_cast<int>(in ? gi : kOut), 0, 0));
+        }
       }
     }
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      if (NT > 1 && !((tiles >> j) & 1u)) continue;
-      u32x4 x[U][Ff::kActs];
+      if (NT > 1 && j >= ntile) break;
+      if constexpr (NT > 1) __builtin_amdgcn_sched_barrier(0);   // one tile's activations at a time: registers
+      u32x4 x[U][kA];
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int g = 0; g < Ff::kActs; ++g) {
-          const int s = sb + u;
-          const bool in = F == Fmt::kW4 ? s * Ff::kK + g * 32 < kend : s * Ff::kK + q * Ff::kLane < kend;
-          x[u][g] = load16(a, in ? aoff[j] : kOut,
-                           static_cast<uint32_t>(s) * (64u * Ff::kActs) + 64u * static_cast<uint32_t>(g));
+        for (int g = 0; g < kA; ++g) {
+          const int k0 = (sb + u) * kK + (is_w4(F) ? mfma_k<F>(g) : 0);
+          const bool in = is_w4(F) ? k0 < kend : k0 + q * lane_k(F) < kend;
+          x[u][g] = load16(a, in ? arow[j] + xq : kOut, static_cast<uint32_t>(k0) * kXe);
         }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         if constexpr (F == Fmt::kF32) {
           const floatx4 xv = __builtin_bit_cast(floatx4, x[u][0]);
-          const floatx4 wv = __builtin_bit_cast(floatx4, w[u]);
-          acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(xv.x, wv.x, acc[j], 0, 0, 0);
-          acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(xv.y, wv.y, acc[j], 0, 0, 0);
-          acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(xv.z, wv.z, acc[j], 0, 0, 0);
-          acc[j] = __builtin_amdgcn_mfma_f32_16x16x4f32(xv.w, wv.w, acc[j], 0, 0, 0);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            const floatx4 wv = __builtin_bit_cast(floatx4, w[u][r]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[j][r] = __builtin_amdgcn_mfma_f32_16x16x4f32(xv[i], wv[i], acc[j][r], 0, 0, 0);
+          }
         } else if constexpr (F == Fmt::kBf16) {
-          acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[u][0]),
-                                                           __builtin_bit_cast(bf16x8, w[u]), acc[j], 0, 0, 0);
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+            acc[j][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[u][0]),
+                                                                __builtin_bit_cast(bf16x8, w[u][r]), acc[j][r], 0, 0, 0);
         } else {
-          // per block of 32 k: sum (128 + q) x - sum (128 + z) x, both products
-          // exact in float32 and the difference formed by the accumulator, then
-          // times the scale
-          u32x4 c = w[u];
-          transpose_quarters(c);
-          uint32_t sg[4];
-          spread_quarters(sc[u], sg);
+          __builtin_amdgcn_sched_barrier(0);
+          constexpr int kG = 128 >> group_shift(F), kPer = 4 / kG;   // groups of a step, MFMAs of a group
+          floatx4 n136[kG];
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const bf16x8 xv = acts_in_code_order(x[u][g]);
-            const uint32_t zz = (sg[g] & 0xffffu) | (sg[g] << 16);
-            const u32x4 z4 = {zz, zz, zz, zz};
-            floatx4 t = {0.f, 0.f, 0.f, 0.f};
-            t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, __builtin_bit_cast(bf16x8, z4), t, 0, 0, 0);
-            t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xv, codes_to_bf16(c[g]), t, 0, 0, 0);
-            const float s = __uint_as_float(sg[g] & 0xffff0000u);
+          for (int g = 0; g < kG; ++g) {
+            n136[g] = floatx4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[j][i] = fmaf(s, t[i], acc[j][i]);
+            for (int i = 0; i < kPer; ++i) {
+              u32x4& xv = x[u][g * kPer + i];
+              if constexpr (!kOrdered) xv = to_code_order(xv);
+              n136[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xv),
+                                                                __builtin_bit_cast(bf16x8, neg), n136[g], 0, 0, 0);
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            if constexpr (RT > 1) __builtin_amdgcn_sched_barrier(0);
+            u32x4 c = w[u][r];
+            // with several tiles the codes are unpacked anew for each: kept
+            // unpacked they would take four times the registers
+            uint32_t sv = sc[u][r];
+            if constexpr (NT > 1) __asm__ volatile("" : "+v"(c.x), "+v"(c.y), "+v"(c.z), "+v"(c.w), "+v"(sv));
+            arrange_codes<F>(c);
+            uint32_t sg[4], zg[4];
+            spread_scales<F>(sv, sg);
+            if constexpr (kZ) spread_scales<F>(zc[u][r], zg);
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
+              floatx4 t = n136[g];
+#pragma unroll
+              for (int i = 0; i < kPer; ++i)
+                t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[u][g * kPer + i]),
+                                                            codes_to_bf16(c[g * kPer + i], base), t, 0, 0, 0);
+              const float s = __uint_as_float(sg[g] << 16);
+              if constexpr (kZ) {
+                const float zf = static_cast<float>(zg[g] & 15u) * (1.f / 136.f) - 8.f / 136.f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) t[i] = fmaf(zf, n136[g][i], t[i]);
+              }
+#pragma unroll
+              for (int i = 0; i < 4; ++i) acc[j][r][i] = fmaf(s, t[i], acc[j][r][i]);
+            }
           }
         }
       }

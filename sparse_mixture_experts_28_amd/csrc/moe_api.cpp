@@ -312,17 +312,17 @@ moe_status_t check_shape_decode(int32_t T, int32_t d, int32_t h, int32_t E, int3
 }
 
 struct DecodeLayout {
-  size_t logits, hid, part, counters, total;
+  size_t logits, xord, hid, part, counters, total;
   int split, ncounter;
 };
 
 DecodeLayout decode_layout(int32_t T, int32_t d, int32_t h, int32_t E, int32_t k, int32_t S, int fmt) {
   DecodeLayout L;
-  const long long row_bytes = fmt == kDecodeF32 ? 4LL * h : fmt == kDecodeBf16 ? 2LL * h : h / 2;
-  L.split = decode_split(T, d, h, E, k, S, row_bytes);
+  L.split = decode_split(T, d, h, E, k, S, fmt);
   L.ncounter = (d + 15) / 16;
   size_t off = 0;
   L.logits = off;   off += align_up(static_cast<size_t>(T) * E * 8);
+  L.xord = off;     off += align_up(fmt == kDecodeW4 ? static_cast<size_t>(T) * d * 2 : 0);
   L.hid = off;      off += align_up(static_cast<size_t>(T) * (k + S) * h * 4);
   L.part = off;     off += align_up(L.split > 1 ? static_cast<size_t>(L.split) * T * d * 4 : 0);
   L.counters = off; off += align_up(static_cast<size_t>(L.ncounter) * 4);
@@ -355,6 +355,7 @@ moe_status_t forward_decode(DecodeArgs a, const moe_launch_t* launch) {
     return MOE_ERR_WORKSPACE;
   char* b = static_cast<char*>(launch->workspace);
   a.logits = reinterpret_cast<double*>(b + L.logits);
+  a.xord = b + L.xord;
   a.hid = b + L.hid;
   a.part = reinterpret_cast<float*>(b + L.part);
   a.counters = reinterpret_cast<int32_t*>(b + L.counters);

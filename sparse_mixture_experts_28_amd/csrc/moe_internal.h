@@ -342,6 +342,7 @@ struct DecodeArgs {
   int32_t* topk_idx;    // [T, k]
   float* topk_w;        // [T, k]
   double* logits;       // [T, E]
+  void* xord;           // 4-bit weights: [T, d] x in the order of the codes
   void* hid;            // [T, k+S] hidden rows times the routing weight: h float32, or h bf16 values and h remainders
   float* part;          // [split, T, d] float32 (split > 1)
   int32_t* counters;    // ncounter, zeroed by the logits kernel
@@ -351,7 +352,7 @@ struct DecodeArgs {
   int fmt;
   int split;            // shares of phase 2's sum per 16 output columns
 };
-int decode_split(int T, int d, int h, int E, int k, int S, long long row_bytes);
+int decode_split(int T, int d, int h, int E, int k, int S, int fmt);
 hipError_t launch_decode(const DecodeArgs& a, hipStream_t st);
 hipError_t launch_w4_quantize(const uint16_t* src, long long n, int gshift, uint8_t* codes, uint16_t* scales,
                               uint8_t* zeros, hipStream_t st);

@@ -94,45 +94,71 @@ __global__ __launch_bounds__(256) void w4_dequantize_kernel(const uint32_t* code
 // ------------------------------------------------------------------ Linear --
 // y[m, n] = sum_k x[m, k] w[n, k] + b[n].  One workgroup per 16 columns and 64
 // rows; its waves split k and add their sums in LDS in wave order.
-template <int NT, int NW>
+template <Fmt F, int NT, int RT, int U, int NW>
 __global__ __launch_bounds__(NW * 64) void w4_linear_kernel(const uint16_t* x, WMat w, const uint16_t* bias,
                                                             uint16_t* y, int M) {
-  __shared__ float red[NT * NW * 256];
-  constexpr int U = 4;
+  __shared__ float red[NT * RT * NW * 256];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int n0 = blockIdx.x * 16, m0 = blockIdx.y * 64;
+  const int n0 = blockIdx.x * 16 * RT, m0 = blockIdx.y * 64;
   const int rows = min(M - m0, 64);
   const uint32_t pitch = static_cast<uint32_t>(w.K) * 2u;
   const __amdgpu_buffer_rsrc_t xr =
       make_rsrc(x + static_cast<size_t>(m0) * w.K, static_cast<uint32_t>(rows) * pitch);
-  uint32_t aoff[NT];
-  floatx4 acc[NT];
+  uint32_t arow[NT];
+  floatx4 acc[NT][RT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int p = j * 16 + (lane & 15);
-    aoff[j] = p < rows ? static_cast<uint32_t>(p) * pitch + 16u * (lane >> 4) : kOut;
-    acc[j] = floatx4{0.f, 0.f, 0.f, 0.f};
+    arow[j] = p < rows ? static_cast<uint32_t>(p) * pitch : kOut;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[j][r] = floatx4{0.f, 0.f, 0.f, 0.f};
   }
   const int tl = (rows + 15) / 16;
   const int nst = (w.K + 127) / 128;
   const int s0 = wave * nst / NW, s1 = (wave + 1) * nst / NW;
-  const WRows wr = rows_of<Fmt::kW4>(w, 0, n0, lane);
-  stream_rows<Fmt::kW4, NT, U>(acc, wr, xr, aoff, (1u << tl) - 1u, s0, s1, w.K, w.gshift, lane);
+  const WRows wr = rows_of<F, RT>(w, 0, n0, lane);
+  if (w.z != nullptr) stream_rows<F, NT, RT, U, false, true>(acc, wr, xr, arow, tl, s0, s1, w.K, lane);
+  else stream_rows<F, NT, RT, U, false, false>(acc, wr, xr, arow, tl, s0, s1, w.K, lane);
 #pragma unroll
   for (int j = 0; j < NT; ++j)
-    *reinterpret_cast<floatx4*>(red + ((j * NW + wave) * 64 + lane) * 4) = acc[j];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+      *reinterpret_cast<floatx4*>(red + (((j * RT + r) * NW + wave) * 64 + lane) * 4) = acc[j][r];
   __syncthreads();
-  for (int i = threadIdx.x; i < tl * 256; i += NW * 64) {
-    const int j = i >> 8, n = i & 15, pr = (i >> 4) & 15;
-    const int p = j * 16 + pr;
+  for (int i = threadIdx.x; i < tl * RT * 256; i += NW * 64) {
+    const int jr = i >> 8, n = (jr % RT) * 16 + (i & 15), pr = (i >> 4) & 15;
+    const int p = jr / RT * 16 + pr;
     if (p >= rows || n0 + n >= w.N) continue;
-    const float* s = red + (j * NW * 64 + (pr >> 2) * 16 + n) * 4 + (pr & 3);
+    const float* s = red + (jr * NW * 64 + (pr >> 2) * 16 + (i & 15)) * 4 + (pr & 3);
     float v = 0.f;
 #pragma unroll
     for (int q = 0; q < NW; ++q) v += s[q * 256];
     if (bias != nullptr) v += bf16_to_f32(bias[n0 + n]);
     y[static_cast<size_t>(m0 + p) * w.N + n0 + n] = f32_to_bf16(v);
   }
+}
+
+#ifndef LRT
+#define LRT 1
+#endif
+#ifndef LU
+#define LU 4
+#endif
+#ifndef LNW
+#define LNW 8
+#endif
+#ifndef LRT4
+#define LRT4 2
+#endif
+#ifndef LU4
+#define LU4 1
+#endif
+template <Fmt F>
+hipError_t launch_linear(const uint16_t* x, int M, const WMat& w, const uint16_t* bias, uint16_t* y, hipStream_t st) {
+  const unsigned gy = (M + 63) / 64;
+  if (M <= 16) w4_linear_kernel<F, 1, LRT, LU, LNW><<<dim3((w.N + 16 * LRT - 1) / (16 * LRT), gy), LNW * 64, 0, st>>>(x, w, bias, y, M);
+  else w4_linear_kernel<F, 4, LRT4, LU4, 8><<<dim3((w.N + 16 * LRT4 - 1) / (16 * LRT4), gy), 512, 0, st>>>(x, w, bias, y, M);
+  return hipGetLastError();
 }
 
 int grid_of(long long n8) {
@@ -161,10 +187,9 @@ hipError_t launch_w4_linear(const uint16_t* x, int M, const uint8_t* codes, cons
                             const uint8_t* zeros, int N, int K, int gshift, const uint16_t* bias, uint16_t* y,
                             hipStream_t st) {
   const WMat w{reinterpret_cast<const char*>(codes), scales, zeros, N, K, 0, gshift};
-  const dim3 grid((N + 15) / 16, (M + 63) / 64);
-  if (M <= 16) w4_linear_kernel<1, 8><<<grid, 512, 0, st>>>(x, w, bias, y, M);
-  else w4_linear_kernel<4, 8><<<grid, 512, 0, st>>>(x, w, bias, y, M);
-  return hipGetLastError();
+  if (gshift == 5) return launch_linear<Fmt::kW4g32>(x, M, w, bias, y, st);
+  if (gshift == 6) return launch_linear<Fmt::kW4g64>(x, M, w, bias, y, st);
+  return launch_linear<Fmt::kW4g128>(x, M, w, bias, y, st);
 }
 
 }  // namespace moe

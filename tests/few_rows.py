@@ -9,8 +9,9 @@ value; a hidden value kept as a bf16 number and its bf16 remainder within
 routing weight (an exponential, a quotient, a product; the logits' difference
 rounded to float32) add at most 2^-18 of the value.
 
-4-bit blocks of 32 form sum (128 + q) x - sum (128 + z) x in float32 before the
-scale: 64 products with factors up to 143, within 64 u 286 sum|x|.
+4-bit groups of up to 128 form sum (128 + q) x - sum 136 x + (8 - z) sum x in
+float32 before the scale: 256 products with factors up to 143, and the last
+term at most 8 / 136 of the second, within 256 u 300 sum|x|.
 """
 import torch
 
@@ -32,7 +33,7 @@ def dot_bound(a, w, w_scale=None):
     n = a.shape[1] + 16
     b = n * U * (a.abs() @ w.abs().t())
     if w_scale is not None:
-        b = b + 64 * U * 286 * (a.abs() @ w_scale.abs().t())
+        b = b + 256 * U * 300 * (a.abs() @ w_scale.abs().t())
     return b
 
 
