@@ -20,6 +20,8 @@
 // output carries one rounding, its own.
 #include "few_rows.h"
 
+#include <cmath>
+
 namespace moe {
 namespace {
 
@@ -158,15 +160,21 @@ __global__ __launch_bounds__(1024) void decode_logits_mfma_kernel(DecodeArgs a) 
 
 // --------------------------------------------------------------- selection --
 // The routing of the call, rebuilt by every workgroup from the logits (a few
-// hundred numbers per token) rather than passed through another launch.
+// hundred numbers per token) rather than passed through another launch.  A job
+// is an expert with up to so many of its tokens as the kernel takes at once; the
+// work is shared out by jobs, so an expert with many tokens (a shared one) does
+// not hold up the wave that meets it.
+constexpr int kMaxRows = kMaxT * (MOE_MAX_TOPK + MOE_MAX_SHARED);
+constexpr int kMaxJobs = kMaxE + kMaxRows / 8;
 struct Routing {
   int idx[kMaxT][MOE_MAX_TOPK];     // expert of slot j, routed slots only
   float w[kMaxT][MOE_MAX_TOPK];
   unsigned long long mask[kMaxE];   // tokens of each expert
-  int list[kMaxE];                  // taken experts, ascending, shared ones last
-  int off[kMaxE + 1];               // first of each one's rows
-  uint16_t row[kMaxT * (MOE_MAX_TOPK + MOE_MAX_SHARED)];   // token + 256 slot, ascending tokens; slot k + s: shared s
-  int n;                            // taken experts
+  uint16_t list[kMaxJobs];          // expert of each job, ascending, shared ones last
+  uint16_t off[kMaxJobs + 1];       // first of its rows
+  uint16_t start[kMaxE];            // first row of each expert
+  uint16_t row[kMaxRows];           // token + 256 slot, ascending tokens; slot k + s: shared s
+  int n;                            // jobs
   uint32_t wsum[kWaves];
 };
 
@@ -204,7 +212,7 @@ __device__ __forceinline__ double wave_max(double v) {
 // One wave, one token: the k largest logits (+ selection bias), ties to the
 // lower expert; a NaN ranks below every number.  Lane l holds experts l,
 // l + 64, l + 128, l + 192.
-__device__ __forceinline__ void select_token(const DecodeArgs& a, Routing& r, int t, int lane, bool write) {
+__device__ __forceinline__ void select_token(const DecodeArgs& a, int t, int lane, int& my_idx, float& my_w) {
   double key[4], val[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -217,7 +225,7 @@ __device__ __forceinline__ void select_token(const DecodeArgs& a, Routing& r, in
   uint32_t left = 0;   // bit i: expert lane + 64 i is there and not taken
 #pragma unroll
   for (int i = 0; i < 4; ++i) left |= lane + 64 * i < a.E ? 1u << i : 0u;
-  int my_idx = 0;
+  my_idx = 0;
   double my_l = -INFINITY, m = -INFINITY;
   for (int j = 0; j < a.k; ++j) {
     double best = -INFINITY;
@@ -252,40 +260,51 @@ __device__ __forceinline__ void select_token(const DecodeArgs& a, Routing& r, in
   float sum = 0.f;
   for (int j = 0; j < a.k; ++j)
     sum += __uint_as_float(__builtin_amdgcn_readlane(static_cast<int>(__float_as_uint(ej)), j));
+  my_w = ej / sum;   // lane j: slot j
+}
+
+__device__ __forceinline__ void write_choice(const DecodeArgs& a, int t, int lane, int idx, float w) {
   if (lane < a.k) {
-    const float w = ej / sum;
-    r.idx[t][lane] = my_idx;
-    r.w[t][lane] = w;
-    if (write) {
-      a.topk_idx[t * a.k + lane] = my_idx;
-      a.topk_w[t * a.k + lane] = w;
-    }
+    a.topk_idx[t * a.k + lane] = idx;
+    a.topk_w[t * a.k + lane] = w;
   }
 }
 
-// Each expert's tokens, the list of the taken experts and their rows, from idx.
-// Thread e handles expert e (at most 264 of 512 threads).
+// One wave per token, for batches whose selection would keep every workgroup of
+// phase 1 busy for long.
+__global__ __launch_bounds__(64) void decode_select_kernel(DecodeArgs a) {
+  int idx;
+  float w;
+  select_token(a, blockIdx.x, threadIdx.x, idx, w);
+  write_choice(a, blockIdx.x, threadIdx.x, idx, w);
+}
+
+// The jobs and their rows from idx, PER tokens at most to a job.
+template <int PER>
 __device__ __forceinline__ void list_routing(const DecodeArgs& a, Routing& r) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = threadIdx.x;
-  const int ne = a.E + a.S, na = a.T * a.k;
-  const unsigned long long all = a.T == 64 ? ~0ull : (1ull << a.T) - 1ull;
-  unsigned long long mask = e >= a.E && e < ne ? all : 0ull;
-  if (na <= 16) {
+  const int ne = a.E + a.S, na = a.T * a.k;   // at most 264 experts (a thread each), 512 choices
+  if (a.T == 1) {   // the order of the experts is free: slot order
+    const int n = a.k + a.S;
     __syncthreads();
-    for (int t = 0; t < a.T; ++t)
-      for (int j = 0; j < a.k; ++j) mask |= r.idx[t][j] == e ? 1ull << t : 0ull;
-  } else {
-    if (e < a.E) r.mask[e] = 0ull;
-    __syncthreads();
-    for (int i = threadIdx.x; i < na; i += kThreads) {
-      const int t = i / a.k, j = i - t * a.k;
-      atomicOr(&r.mask[r.idx[t][j]], 1ull << t);   // a set: the order does not matter
+    if (e <= n) {
+      r.list[e] = static_cast<uint16_t>(e < a.k ? r.idx[0][e] : a.E + e - a.k);
+      r.off[e] = static_cast<uint16_t>(e);
+      r.row[e] = static_cast<uint16_t>(e << 8);
     }
+    if (e == 0) r.n = n;
     __syncthreads();
-    if (e < a.E) mask = r.mask[e];
+    return;
   }
-  // prefix sums of (taken, rows), in two halves of a word
-  const uint32_t own = mask != 0ull ? 0x10000u + __popcll(mask) : 0u;
+  if (e < ne) r.mask[e] = e < a.E ? 0ull : a.T == 64 ? ~0ull : (1ull << a.T) - 1ull;
+  __syncthreads();
+  const int t = e / a.k, j = e - t * a.k;     // the thread's choice
+  const int mine = e < na ? r.idx[t][j] : 0;
+  if (e < na) atomicOr(&r.mask[mine], 1ull << t);   // a set: the order does not matter
+  __syncthreads();
+  const int cnt = e < ne ? __popcll(r.mask[e]) : 0;
+  // prefix sums of (jobs, rows), in two halves of a word
+  const uint32_t own = (static_cast<uint32_t>((cnt + PER - 1) / PER) << 16) + cnt;
   uint32_t sc = own;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
@@ -295,47 +314,61 @@ __device__ __forceinline__ void list_routing(const DecodeArgs& a, Routing& r) {
   if (lane == 63) r.wsum[wave] = sc;
   __syncthreads();
   uint32_t before = sc - own, total = 0;
+#pragma unroll
   for (int w = 0; w < kWaves; ++w) {
-    if (w < wave) before += r.wsum[w];
-    total += r.wsum[w];
+    const uint32_t v = r.wsum[w];
+    if (w < wave) before += v;
+    total += v;
   }
-  if (mask != 0ull) {
-    const int pos = before >> 16;
-    int o = before & 0xffffu;
-    r.list[pos] = e;
-    r.off[pos] = o;
-    while (mask != 0ull) {
-      const int t = __ffsll(static_cast<long long>(mask)) - 1;
-      mask &= mask - 1ull;
-      int slot = a.k + e - a.E;
-      if (e < a.E) {
-        slot = 0;
-        for (int i = 1; i < a.k; ++i) slot = r.idx[t][i] == e ? i : slot;
-      }
-      r.row[o++] = static_cast<uint16_t>(t | (slot << 8));
-    }
+  const int o = before & 0xffffu;
+  for (int i = 0, pos = before >> 16; i < cnt; i += PER, ++pos) {
+    r.list[pos] = static_cast<uint16_t>(e);
+    r.off[pos] = static_cast<uint16_t>(o + i);
   }
-  if (threadIdx.x == 0) {
+  if (e < ne) r.start[e] = static_cast<uint16_t>(o);
+  if (e == 0) {
     r.n = total >> 16;
-    r.off[total >> 16] = total & 0xffffu;
+    r.off[total >> 16] = static_cast<uint16_t>(total & 0xffffu);
+  }
+  __syncthreads();
+  // a choice's row: behind the expert's earlier tokens
+  if (e < na) {
+    const int at = r.start[mine] + __popcll(r.mask[mine] & ((1ull << t) - 1ull));
+    r.row[at] = static_cast<uint16_t>(t | (j << 8));
+  }
+  for (int i = e; i < a.S * a.T; i += kThreads) {
+    const int s = i / a.T, ts = i - s * a.T;
+    r.row[r.start[a.E + s] + ts] = static_cast<uint16_t>(ts | ((a.k + s) << 8));
   }
   __syncthreads();
 }
 
-// from the logits
+// from the logits, a wave per token (T <= kWaves)
+template <int PER>
 __device__ __forceinline__ void build_routing(const DecodeArgs& a, Routing& r, bool write) {
-  for (int t = threadIdx.x >> 6; t < a.T; t += kWaves) select_token(a, r, t, threadIdx.x & 63, write);
-  list_routing(a, r);
+  const int lane = threadIdx.x & 63, t = threadIdx.x >> 6;
+  if (t < a.T) {
+    int idx;
+    float w;
+    select_token(a, t, lane, idx, w);
+    if (lane < a.k) {
+      r.idx[t][lane] = idx;
+      r.w[t][lane] = w;
+    }
+    if (write) write_choice(a, t, lane, idx, w);
+  }
+  list_routing<PER>(a, r);
 }
 
-// from the experts and weights that phase 1 left in the outputs
+// from the experts and weights in the outputs
+template <int PER>
 __device__ __forceinline__ void load_routing(const DecodeArgs& a, Routing& r) {
-  for (int i = threadIdx.x; i < a.T * a.k; i += kThreads) {
-    const int t = i / a.k, j = i - t * a.k;
+  const int i = threadIdx.x, t = i / a.k, j = i - t * a.k;
+  if (i < a.T * a.k) {
     r.idx[t][j] = a.topk_idx[i];
     r.w[t][j] = a.topk_w[i];
   }
-  list_routing(a, r);
+  list_routing<PER>(a, r);
 }
 
 template <bool BF16>
@@ -363,54 +396,167 @@ __device__ __forceinline__ void stores_done() {
   __asm__ volatile("" ::: "memory");
 }
 
+// Items of a phase go to its workgroups in turn or, where a workgroup has
+// megabytes to read (DecodeArgs::dynamic), as they come free: the first by number,
+// the others by a counter, asked for while the item before is under way.  Waves
+// see memory at uneven rates, and jobs with many tokens cost more: in turn, the
+// second phase of the DeepSeek-shaped layer (32 tokens) took 1030 us, its
+// workgroups ending between 605 and 1106; by the counter 825.  Short items lose:
+// the counter's answer arrives among the weight loads (Mixtral shape, one token,
+// 128 KB items: 42.9 us in turn, 46.7 by the counter).
+struct Tickets {
+  int32_t* counter;
+  int* slot;       // two words of LDS, used in turn
+  bool dynamic;
+  int turn, next;
+  __device__ __forceinline__ void ask(int i) {
+    next = i + gridDim.x;
+    if (dynamic && threadIdx.x == 0) next = gridDim.x + atomicAdd(counter, 1);
+  }
+  // between ask() and take(), before a barrier
+  __device__ __forceinline__ void publish() {
+    if (threadIdx.x == 0) slot[turn] = next;
+  }
+  __device__ __forceinline__ int take() {
+    const int i = slot[turn];
+    turn ^= 1;
+    return uniform(i);
+  }
+};
+
+#ifndef A_RT
+#define A_RT 1
+#endif
+#ifndef A_U
+#define A_U 4
+#endif
+#ifndef B_U
+#define B_U 4
+#endif
+#ifndef M_U
+#define M_U 2
+#endif
+#ifndef MB_U
+#define MB_U 4
+#endif
+#ifndef B64NT
+#define B64NT 3
+#endif
+#ifndef WGS
+#define WGS 2
+#endif
+// Shapes of the phase kernels by format and token class: row tiles of a wave,
+// steps loaded together, tiles of tokens at once (an expert with more makes
+// several jobs), bytes of a wave's activation region, workgroups per CU.
+template <Fmt F, int TMAX> struct Shape {
+  static constexpr bool kW = is_w4(F), kMany = TMAX > 16;
+  static constexpr int kRT1 = kW && !kMany ? A_RT : 1;
+  static constexpr int kRT2 = kRT1;
+  static constexpr int kU = kW ? (kMany ? M_U : A_U) : kMany ? MB_U : B_U;
+  static constexpr int kNT1 = !kMany || kW ? 1 : 2;
+  static constexpr int kNT2 = kW ? 1 : F == Fmt::kF32 ? kNT1 : TMAX == 1 ? 1 : TMAX == 16 ? 2 : B64NT;
+  static constexpr int kRows1 = TMAX == 1 ? 1 : 16 * kNT1, kRows2 = TMAX == 1 ? (F == Fmt::kF32 ? 1 : 2) : 16 * kNT2;
+  static constexpr int kRows = kRows1 > kRows2 ? kRows1 : kRows2;   // most rows staged
+  static constexpr int kStep = kW ? 256 : 64;
+  static constexpr int kStage = (TMAX == 1 ? (kW ? 2048 : 1024) : kRows * (kStep + 16)) + 32 + kStageZero;
+  static constexpr int kWgs = WGS;
+};
+
+// a segment's products for one tile of tokens or for all NT (the others then
+// hold rows whose sums nobody reads)
+template <int NT, int RT, typename St, typename SlotOff>
+__device__ __forceinline__ void run_tiles(St& st, floatx4 (&acc)[NT][RT], __amdgpu_buffer_rsrc_t a, SlotOff soff,
+                                          const int (&rslot)[NT], int tl, char* stage, int lane) {
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < RT; ++i) acc[j][i] = floatx4{0.f, 0.f, 0.f, 0.f};
+  if (NT > 1 && tl == 1) {
+    floatx4 one[1][RT];
+    const int rs[1] = {rslot[0]};
+#pragma unroll
+    for (int i = 0; i < RT; ++i) one[0][i] = acc[0][i];
+    st.run(one, a, soff, rs, stage, lane);
+#pragma unroll
+    for (int i = 0; i < RT; ++i) acc[0][i] = one[0][i];
+  } else {
+    st.run(acc, a, soff, rslot, stage, lane);
+  }
+}
+
 // ------------------------------------------------------------------ phase 1 --
-// One item: taken expert number ai and 16 RT hidden units from n0.  The expert's
-// tokens are the activation rows, NT tiles of 16; the waves split k and add
-// their sums in LDS in wave order.
-template <Fmt F, int NT, int RT, int U>
-__device__ void phase1_item(const DecodeArgs& a, Routing& r, float* red, int ai, int n0) {
+// One item: a job and 16 RT hidden units.  The job's tokens are the activation
+// rows, NT tiles of 16; the waves split k and add their sums in LDS in wave
+// order.  The next item's first loads are issued before this one's sums, biases,
+// activations and stores.
+template <Fmt F, int TMAX>
+__global__ __launch_bounds__(kThreads, 4) void decode_phase1_kernel(DecodeArgs a) {
+  using Sh = Shape<F, TMAX>;
   constexpr bool kBf = F != Fmt::kF32;
+  constexpr int NT = Sh::kNT1, RT = Sh::kRT1, U = Sh::kU, kN = 16 * RT;
+  using St = Stream<F, RT, U, true, Sh::kRows, Sh::kStage>;
+  __shared__ Routing r;
+  __shared__ float red[NT * RT * kWaves * 256];
+  __shared__ __attribute__((aligned(16))) char stages[kWaves][Sh::kStage];
+  __shared__ int next[2];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int e = uniform(r.list[ai]), o = uniform(r.off[ai]);
-  const int rows = uniform(r.off[ai + 1]) - o;
-  const uint32_t pitch = static_cast<uint32_t>(a.d) * (kBf ? 2u : 4u);
+  char* stage = stages[wave];
+  St::clear(stage, lane);
+  if (TMAX <= 16 && a.T <= kWaves) build_routing<16 * NT>(a, r, blockIdx.x == 0);
+  else load_routing<16 * NT>(a, r);
+
+  const int ntile = (a.h + kN - 1) / kN;
+  const int items = uniform(r.n) * ntile;
+  const int nst = (a.d + step_k(F) - 1) / step_k(F), nb = (nst + U - 1) / U;
+  const int s0 = wave * nb / kWaves * U, s1 = min(nst, (wave + 1) * nb / kWaves * U);
+  const uint32_t pitch = static_cast<uint32_t>(a.d) * act_bytes(F);
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(is_w4(F) ? a.xord : a.x, static_cast<uint32_t>(a.T) * pitch);
-  const int nst = (a.d + step_k(F) - 1) / step_k(F);
-  const int s0 = wave * nst / kWaves, s1 = (wave + 1) * nst / kWaves;
-  const WRows wr = rows_of<F, RT>(a.W1, e, n0, lane);
-  for (int p0 = 0; p0 < rows; p0 += 16 * NT) {
-    uint32_t arow[NT];
+  Tickets tk{a.counters, next, a.dynamic != 0, 0, 0};
+  St st;
+  int e = 0, n0 = 0, o = 0, rows = 0;   // the item's expert, first hidden unit, first row and rows
+  auto soff = [&](int slot) { return static_cast<uint32_t>(r.row[o + slot] & 255) * pitch; };
+  auto begin = [&](int item) {
+    const int job = item / ntile;
+    e = uniform(r.list[job]);
+    n0 = (item - job * ntile) * kN;
+    o = uniform(r.off[job]);
+    rows = uniform(r.off[job + 1]) - o;
+    st.begin(rows_of<F, RT>(a.W1, e, n0, lane), xr, soff, rows, s0, s1, a.d, lane);
+  };
+  int item = blockIdx.x;
+  if (item < items) begin(item);
+  while (item < items) {
+    tk.ask(item);
+    const int tl = (rows + 15) / 16;
+    int rslot[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) rslot[j] = min(j * 16 + (lane & 15), rows - 1);
     floatx4 acc[NT][RT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int p = p0 + j * 16 + (lane & 15);
-      arow[j] = p < rows ? static_cast<uint32_t>(r.row[o + p] & 255) * pitch : kOut;
-#pragma unroll
-      for (int i = 0; i < RT; ++i) acc[j][i] = floatx4{0.f, 0.f, 0.f, 0.f};
-    }
-    const int tl = min(NT, (rows - p0 + 15) / 16);
-    if (is_w4(F) && a.W1.z != nullptr) stream_rows<F, NT, RT, U, true, true>(acc, wr, xr, arow, tl, s0, s1, a.d, lane);
-    else stream_rows<F, NT, RT, U, true, false>(acc, wr, xr, arow, tl, s0, s1, a.d, lane);
+    run_tiles(st, acc, xr, soff, rslot, tl, stage, lane);
 #pragma unroll
     for (int j = 0; j < NT; ++j)
-      if (NT == 1 || j < tl) {
+      if (j < tl) {
 #pragma unroll
         for (int i = 0; i < RT; ++i)
           *reinterpret_cast<floatx4*>(red + (((j * RT + i) * kWaves + wave) * 64 + lane) * 4) = acc[j][i];
       }
+    tk.publish();
     __syncthreads();
+    const int ce = e, cn0 = n0, co = o, crows = rows;
+    item = tk.take();
+    if (item < items) begin(item);
     for (int i = threadIdx.x; i < tl * RT * 256; i += kThreads) {
-      // result (row p of the expert's tokens, hidden unit n): lane (n, p / 4 % 4), register p % 4
-      const int jr = i >> 8, n = n0 + (jr % RT) * 16 + (i & 15), pr = (i >> 4) & 15;
-      const int p = p0 + jr / RT * 16 + pr;
-      if (p >= rows || n >= a.h) continue;
-      const float* s = red + (jr * kWaves * 64 + (pr >> 2) * 16 + (i & 15)) * 4 + (pr & 3);
+      // result (row p of the job's tokens, hidden unit n): lane (n, p / 4 % 4), register p % 4
+      const int jr = i >> 8, n = cn0 + (jr % RT) * 16 + (i & 15), pr = (i >> 4) & 15;
+      const int p = jr / RT * 16 + pr;
+      if (p >= crows || n >= a.h) continue;
+      const float* sum = red + (jr * kWaves * 64 + (pr >> 2) * 16 + (i & 15)) * 4 + (pr & 3);
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) v += s[w * 256];
-      if (a.b1 != nullptr) v += load1<kBf>(a.b1, static_cast<size_t>(e) * a.h + n);
+      for (int w = 0; w < kWaves; ++w) v += sum[w * 256];
+      if (a.b1 != nullptr) v += load1<kBf>(a.b1, static_cast<size_t>(ce) * a.h + n);
       v = a.act == MOE_ACT_SILU ? v / (1.f + expf(-v)) : 0.5f * v * (1.f + erff(v * 0.70710678118654752440f));
-      const int t = r.row[o + p] & 255, slot = r.row[o + p] >> 8;
+      const int t = r.row[co + p] & 255, slot = r.row[co + p] >> 8;
       if (slot < a.k) v *= r.w[t][slot];
       const size_t row = static_cast<size_t>(t) * (a.k + a.S) + slot;
       if constexpr (kBf) {
@@ -425,7 +571,7 @@ __device__ void phase1_item(const DecodeArgs& a, Routing& r, float* red, int ai,
         static_cast<float*>(a.hid)[row * a.h + n] = v;
       }
     }
-    __syncthreads();   // red is written again
+    __syncthreads();   // red is written again by the next item
   }
 }
 
@@ -445,55 +591,90 @@ __device__ __forceinline__ void write_out(const DecodeArgs& a, const Routing& r,
   else static_cast<float*>(a.out)[o] = v;
 }
 
-// One item: 16 RT output columns from n0 over share sp of the summed range, all
-// taken experts' k one after the other.  An expert's tokens are the activation
-// rows (bf16: tiles of 8 tokens, rows 0..7 their hidden values, 8..15 the
-// remainders; float32: tiles of 16), so an expert with one token costs one
-// MFMA, and its sums go to its tokens only.  Each wave adds them to a table of
-// its own in LDS, [T][16 RT]; the tables are added in wave order at the end.
-template <Fmt F, int NT, int RT, int U, int TMAX>
-__device__ void phase2_item(const DecodeArgs& a, Routing& r, float* tab, int* flag, int tile, int sp) {
+// One item: 16 RT output columns over a share of the summed range, all jobs' k
+// one after the other.  A job's tokens are the activation rows (bf16: tiles of 8
+// tokens, rows 0..7 their hidden values, 8..15 the remainders; float32: tiles of
+// 16), so an expert with one token costs one MFMA, and its sums go to its tokens
+// only.  Each wave adds them to a table of its own in LDS, [T][16 RT]; the tables
+// are added in wave order at the end.  Loads run ahead as in phase 1: the next
+// job's before a job's sums, the next item's before an item's.
+template <Fmt F, int TMAX>
+__global__ __launch_bounds__(kThreads, 4) void decode_phase2_kernel(DecodeArgs a) {
+  using Sh = Shape<F, TMAX>;
   constexpr bool kBf = F != Fmt::kF32;
   constexpr int kTok = kBf ? 8 : 16;
-  constexpr int kN = 16 * RT;
+  constexpr int NT = Sh::kNT2, RT = Sh::kRT2, U = Sh::kU, kN = 16 * RT;
+  using St = Stream<F, RT, U, true, Sh::kRows, Sh::kStage>;
+  __shared__ Routing r;
+  __shared__ float tab[kWaves][TMAX * kN];
+  __shared__ __attribute__((aligned(16))) char stages[kWaves][Sh::kStage];
+  __shared__ int next[2];
+  __shared__ int flag;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int n0 = tile * kN;
-  const int nst = (a.h + step_k(F) - 1) / step_k(F);
-  const int na = uniform(r.n);
-  const int total = na * nst;   // at most 264 * 2^16
-  const int share = sp * kWaves + wave, shares = a.split * kWaves;
-  int f = static_cast<int>(static_cast<long long>(total) * share / shares);
-  const int fend = static_cast<int>(static_cast<long long>(total) * (share + 1) / shares);
-  float* mine = tab + wave * TMAX * kN;
-  for (int i = lane; i < a.T * kN; i += 64) mine[i] = 0.f;
-  const uint32_t pitch = static_cast<uint32_t>(a.h) * (kBf ? 2u : 4u);
+  char* stage = stages[wave];
+  float* mine = tab[wave];
+  St::clear(stage, lane);
+  load_routing<kTok * NT>(a, r);
+
+  const int tiles = (a.d + kN - 1) / kN;
+  const int items = tiles * a.split;
+  const int nst = (a.h + step_k(F) - 1) / step_k(F), nb = (nst + U - 1) / U;   // steps and batches of a job
+  const int total = uniform(r.n) * nb;   // at most 392 * 2^16
+  const int shares = a.split * kWaves;
+  const uint32_t pitch = static_cast<uint32_t>(a.h) * act_bytes(F);
   const uint32_t rowb = kBf ? 2u * pitch : pitch;
   const __amdgpu_buffer_rsrc_t hr =
       make_rsrc(a.hid, static_cast<uint32_t>(a.T) * static_cast<uint32_t>(a.k + a.S) * rowb);
-  int ai = f / nst, s0 = f - ai * nst;
-  while (f < fend) {
-    const int s1 = min(nst, s0 + fend - f);
-    const int e = uniform(r.list[ai]), o = uniform(r.off[ai]);
-    const int rows = uniform(r.off[ai + 1]) - o;
-    const WRows wr = rows_of<F, RT>(a.W2, e, n0, lane);
-    for (int p0 = 0; p0 < rows; p0 += kTok * NT) {
-      const int tl = min(NT, (rows - p0 + kTok - 1) / kTok);
-      uint32_t arow[NT];
-      floatx4 acc[NT][RT];
+  Tickets tk{a.counters + 1, next, a.dynamic != 0, 0, 0};
+  St st;
+  int n0 = 0, f = 0, fend = 0;            // the item's first column; the wave's batches left of it
+  int job = 0, b0 = 0, o = 0, rows = 0;   // the segment's job, first batch, first row and rows
+  auto soff = [&](int slot) {
+    const int p = kBf && slot >= rows ? slot - rows : slot;
+    const int ts = r.row[o + p];
+    return (static_cast<uint32_t>(ts & 255) * (a.k + a.S) + (ts >> 8)) * rowb + (p != slot ? pitch : 0u);
+  };
+  auto begin = [&]() {   // the segment of job `job` from batch b0 on
+    const int n = min(nb - b0, fend - f);
+    f += n;
+    o = uniform(r.off[job]);
+    rows = uniform(r.off[job + 1]) - o;
+    st.begin(rows_of<F, RT>(a.W2, uniform(r.list[job]), n0, lane), hr, soff, kBf ? 2 * rows : rows, b0 * U,
+             min(nst, (b0 + n) * U), a.h, lane);
+  };
+  auto begin_item = [&](int item) {
+    const int sp = item / tiles;
+    n0 = (item - sp * tiles) * kN;
+    const int share = sp * kWaves + wave;
+    f = static_cast<int>(static_cast<long long>(total) * share / shares);
+    fend = static_cast<int>(static_cast<long long>(total) * (share + 1) / shares);
+    job = f / nb;
+    b0 = f - job * nb;
+    if (f < fend) begin();
+    else rows = 0;
+  };
+  int item = blockIdx.x;
+  if (item < items) begin_item(item);
+  while (item < items) {
+    tk.ask(item);
+    for (int i = lane; i < a.T * kN; i += 64) mine[i] = 0.f;
+    while (rows > 0) {
+      const int tl = (rows + kTok - 1) / kTok;
+      int rslot[NT];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const int p = p0 + j * kTok + (lane & (kTok - 1));
-        arow[j] = kOut;
-        if (p < rows) {
-          const int ts = r.row[o + p];
-          arow[j] = (static_cast<uint32_t>(ts & 255) * (a.k + a.S) + (ts >> 8)) * rowb;
-          if (kBf && (lane & 8)) arow[j] += pitch;
-        }
-#pragma unroll
-        for (int i = 0; i < RT; ++i) acc[j][i] = floatx4{0.f, 0.f, 0.f, 0.f};
+        rslot[j] = min(j * kTok + (lane & (kTok - 1)), rows - 1);
+        if (kBf && (lane & 8)) rslot[j] += rows;
       }
-      if (is_w4(F) && a.W2.z != nullptr) stream_rows<F, NT, RT, U, true, true>(acc, wr, hr, arow, tl, s0, s1, a.h, lane);
-      else stream_rows<F, NT, RT, U, true, false>(acc, wr, hr, arow, tl, s0, s1, a.h, lane);
+      floatx4 acc[NT][RT];
+      run_tiles(st, acc, hr, soff, rslot, tl, stage, lane);
+      const int co = o, crows = rows;
+      rows = 0;
+      if (f < fend) {
+        ++job;
+        b0 = 0;
+        begin();
+      }
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         if (NT > 1 && j >= tl) break;
@@ -506,128 +687,70 @@ __device__ void phase2_item(const DecodeArgs& a, Routing& r, float* tab, int* fl
               auto hl = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
               v = __uint_as_float(hl[0]) + __uint_as_float(hl[1]);
             }
-            const int p = p0 + j * kTok + (lane >> 4) * 4 + m;
-            if (p < rows && (!kBf || lane < 32)) mine[(r.row[o + p] & 255) * kN + i * 16 + (lane & 15)] += v;
+            const int p = j * kTok + (lane >> 4) * 4 + m;
+            if (p < crows && (!kBf || lane < 32)) mine[(r.row[co + p] & 255) * kN + i * 16 + (lane & 15)] += v;
           }
       }
     }
-    f += s1 - s0;
-    s0 = 0;
-    ++ai;
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < a.T * kN; i += kThreads) {
-    const int t = i / kN, n = n0 + i % kN;
-    if (n >= a.d) continue;
-    float v = 0.f;
+    tk.publish();
+    __syncthreads();
+    const int cn0 = n0, sp = item / tiles, tile = item - sp * tiles;
+    item = tk.take();
+    if (item < items) begin_item(item);
+    for (int i = threadIdx.x; i < a.T * kN; i += kThreads) {
+      const int t = i / kN, n = cn0 + i % kN;
+      if (n >= a.d) continue;
+      float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += tab[w * TMAX * kN + i];
-    if (a.split > 1) store_agent(a.part + (static_cast<size_t>(sp) * a.T + t) * a.d + n, v);
-    else write_out<kBf>(a, r, t, n, v);
-  }
-  if (a.split > 1) {
-    // the last share of the tile to arrive adds all of them, in share order
-    stores_done();
-    __syncthreads();
-    if (threadIdx.x == 0) *flag = atomicAdd(&a.counters[tile], 1) == a.split - 1;
-    __syncthreads();
-    if (*flag) {
-      for (int i = threadIdx.x; i < a.T * kN; i += kThreads) {
-        const int t = i / kN, n = n0 + i % kN;
-        if (n >= a.d) continue;
-        float v = 0.f;
-        for (int q = 0; q < a.split; ++q) v += load_agent(a.part + (static_cast<size_t>(q) * a.T + t) * a.d + n);
-        write_out<kBf>(a, r, t, n, v);
+      for (int w = 0; w < kWaves; ++w) v += tab[w][i];
+      if (a.split > 1) store_agent(a.part + (static_cast<size_t>(sp) * a.T + t) * a.d + n, v);
+      else write_out<kBf>(a, r, t, n, v);
+    }
+    if (a.split > 1) {
+      // the last share of the tile to arrive adds all of them, in share order
+      stores_done();
+      __syncthreads();
+      if (threadIdx.x == 0) flag = atomicAdd(&a.counters[2 + tile], 1) == a.split - 1;
+      __syncthreads();
+      if (flag) {
+        for (int i = threadIdx.x; i < a.T * kN; i += kThreads) {
+          const int t = i / kN, n = cn0 + i % kN;
+          if (n >= a.d) continue;
+          float v = 0.f;
+          for (int q0 = 0; q0 < a.split; q0 += 8) {   // eight loads in flight
+            float p[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              p[q] = load_agent(a.part + (static_cast<size_t>(min(q0 + q, a.split - 1)) * a.T + t) * a.d + n);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v += q0 + q < a.split ? p[q] : 0.f;
+          }
+          write_out<kBf>(a, r, t, n, v);
+        }
       }
     }
+    __syncthreads();   // tab and flag are written again by the next item
   }
-  __syncthreads();   // tab and flag are written again by the next item
 }
 
-#ifndef RTB
-#define RTB 1
-#endif
-#ifndef RTW
-#define RTW 4
-#endif
-#ifndef UB
-#define UB 8
-#endif
-#ifndef UW
-#define UW 4
-#endif
-#ifndef RTB2
-#define RTB2 RTB
-#endif
-#ifndef RTW2
-#define RTW2 RTW
-#endif
-#ifndef W4NT
-#define W4NT 2
-#endif
-#ifndef RT64
-#define RT64 1
-#endif
-#ifndef UW64
-#define UW64 2
-#endif
-#ifndef WG1
-#define WG1 2
-#endif
-#ifndef WG2
-#define WG2 2
-#endif
-// Row tiles of a wave and the steps it loads together: 4 to 16 KB in flight.
-template <Fmt F, int TMAX> struct Shape {
-  static constexpr int kRT1 = TMAX > 16 ? (is_w4(F) ? RT64 : 1) : is_w4(F) ? RTW : RTB;
-  static constexpr int kRT2 = TMAX > 16 ? (is_w4(F) ? RT64 : 1) : is_w4(F) ? RTW2 : RTB2;
-  static constexpr int kB = TMAX > 16 ? (is_w4(F) ? UW64 : 4) : is_w4(F) ? UW : UB;
-  static constexpr int kU1 = kB / kRT1 > 0 ? kB / kRT1 : 1;
-  static constexpr int kU2 = kB / kRT2 > 0 ? kB / kRT2 : 1;
-  // tiles of tokens at once; 4-bit: experts with more tokens are streamed again
-  static constexpr int kNT1 = is_w4(F) ? (TMAX > 16 ? W4NT : 1) : (TMAX + 15) / 16;
-  static constexpr int kNT2 = is_w4(F) ? kNT1 : F == Fmt::kF32 ? kNT1 : (TMAX + 7) / 8;
-};
-
-template <Fmt F, int TMAX>
-__global__ __launch_bounds__(kThreads) void decode_phase1_kernel(DecodeArgs a) {
-  using Sh = Shape<F, TMAX>;
-  __shared__ Routing r;
-  __shared__ float red[Sh::kNT1 * Sh::kRT1 * kWaves * 256];
-  build_routing(a, r, blockIdx.x == 0);
-  constexpr int kN = 16 * Sh::kRT1;
-  const int ntile = (a.h + kN - 1) / kN;
-  const int items = uniform(r.n) * ntile;
-  for (int i = blockIdx.x; i < items; i += gridDim.x)
-    phase1_item<F, Sh::kNT1, Sh::kRT1, Sh::kU1>(a, r, red, i / ntile, i % ntile * kN);
-}
-
-template <Fmt F, int TMAX>
-__global__ __launch_bounds__(kThreads) void decode_phase2_kernel(DecodeArgs a) {
-  using Sh = Shape<F, TMAX>;
-  __shared__ Routing r;
-  __shared__ float tab[kWaves * TMAX * 16 * Sh::kRT2];
-  __shared__ int flag;
-  load_routing(a, r);
-  const int items = (a.d + 16 * Sh::kRT2 - 1) / (16 * Sh::kRT2) * a.split;
-  for (int i = blockIdx.x; i < items; i += gridDim.x)
-    phase2_item<F, Sh::kNT2, Sh::kRT2, Sh::kU2, TMAX>(a, r, tab, &flag, i / a.split, i % a.split);
-}
-
-template <Fmt F, int TMAX>
+// F: the format without zero points, Z: with them (the same where there are none)
+template <Fmt F, Fmt Z, int TMAX>
 hipError_t launch_phases(const DecodeArgs& a, hipStream_t st) {
-  const int cus = device_cu_count();
-  decode_phase1_kernel<F, TMAX><<<cus * WG1, kThreads, 0, st>>>(a);
-  const hipError_t e = hipGetLastError();
+  const int grid = device_cu_count() * Shape<F, TMAX>::kWgs;
+  if (a.T > kWaves) decode_select_kernel<<<a.T, 64, 0, st>>>(a);
+  if (a.W1.z != nullptr) decode_phase1_kernel<Z, TMAX><<<grid, kThreads, 0, st>>>(a);
+  else decode_phase1_kernel<F, TMAX><<<grid, kThreads, 0, st>>>(a);
+  const hipError_t e = hipGetLastError();   // of either launch: a failed one is remembered
   if (e != hipSuccess) return e;
-  decode_phase2_kernel<F, TMAX><<<cus * WG2, kThreads, 0, st>>>(a);
+  if (a.W2.z != nullptr) decode_phase2_kernel<Z, TMAX><<<grid, kThreads, 0, st>>>(a);
+  else decode_phase2_kernel<F, TMAX><<<grid, kThreads, 0, st>>>(a);
   return hipGetLastError();
 }
-template <Fmt F>
+template <Fmt F, Fmt Z>
 hipError_t launch_phases(const DecodeArgs& a, hipStream_t st) {
-  if (a.T <= 8) return launch_phases<F, 8>(a, st);
-  if (a.T <= 16) return launch_phases<F, 16>(a, st);
-  return launch_phases<F, kMaxT>(a, st);
+  if (a.T == 1) return launch_phases<F, Z, 1>(a, st);
+  if (a.T <= 16) return launch_phases<F, Z, 16>(a, st);
+  return launch_phases<F, Z, kMaxT>(a, st);
 }
 
 template <bool BF16>
@@ -640,35 +763,36 @@ void launch_logits(const DecodeArgs& a, hipStream_t st) {
 }
 
 template <Fmt F>
-int row_tiles2(int T) {
-  return T <= 8 ? Shape<F, 8>::kRT2 : T <= 16 ? Shape<F, 16>::kRT2 : Shape<F, kMaxT>::kRT2;
+int phase2_shape(int T, int* wgs) {
+  *wgs = T == 1 ? Shape<F, 1>::kWgs : T <= 16 ? Shape<F, 16>::kWgs : Shape<F, kMaxT>::kWgs;
+  return T == 1 ? Shape<F, 1>::kRT2 : T <= 16 ? Shape<F, 16>::kRT2 : Shape<F, kMaxT>::kRT2;
 }
 
 }  // namespace
 
-// Shares of phase 2's sum per tile of output columns: as few as fill whole
-// rounds of the grid, at least 32 KB of weights in each.
-int decode_split(int T, int d, int h, int E, int k, int S, int fmt) {
-  const int rt = fmt == kDecodeF32 ? row_tiles2<Fmt::kF32>(T) : fmt == kDecodeBf16 ? row_tiles2<Fmt::kBf16>(T)
-                                                                                  : row_tiles2<Fmt::kW4g128>(T);
-  const long long tiles = (d + 16 * rt - 1) / (16 * rt);
-  long long used = static_cast<long long>(T) * k;
-  if (used > E) used = E;
-  used += S;
-  const long long row_bytes = fmt == kDecodeF32 ? 4LL * h : fmt == kDecodeBf16 ? 2LL * h : h / 2;
-  const long long bytes = used * 16 * rt * row_bytes;   // of one tile
-  long long best = 1;
-  double eff = 0;
-  for (long long sp = 1; sp <= 64; ++sp) {
-    if (sp > 1 && bytes / sp < 32768) break;
-    const double rounds = static_cast<double>(tiles * sp) / (256 * WG2);
-    const double full = rounds / static_cast<double>(static_cast<long long>(rounds + 0.999999));
-    if (full > eff + 0.02) {
-      eff = full;
-      best = sp;
-    }
-  }
-  return static_cast<int>(best);
+// How a call's work is shared out; from the sizes alone, with the experts that
+// are taken when T tokens take k of E evenly.
+//   split    phase 2: shares of the sum per tile of output columns, one round of
+//            the grid or items of 1 MB, whichever makes more, of 32 KB at least
+//            and 64 at most
+//   dynamic  2 MB or more to read per workgroup and phase
+DecodePlan decode_plan(int T, int d, int h, int E, int k, int S, int fmt) {
+  int wgs = 0;
+  const int rt = fmt == kDecodeF32 ? phase2_shape<Fmt::kF32>(T, &wgs)
+                                   : fmt == kDecodeBf16 ? phase2_shape<Fmt::kBf16>(T, &wgs)
+                                                        : phase2_shape<Fmt::kW4g128>(T, &wgs);
+  const double used = E * (1.0 - std::pow(1.0 - static_cast<double>(k) / E, T)) + S;
+  const double elem = fmt == kDecodeF32 ? 4.0 : fmt == kDecodeBf16 ? 2.0 : 0.5;
+  const int tiles = (d + 16 * rt - 1) / (16 * rt);
+  const double tile_bytes = used * 16 * rt * h * elem;
+  const int slots = 256 * wgs;
+  int sp = (slots + tiles - 1) / tiles;
+  const double by_size = tile_bytes / (1 << 20);
+  if (sp < by_size) sp = by_size < 64.0 ? static_cast<int>(by_size) : 64;
+  const double most = tile_bytes / 32768;
+  if (sp > most) sp = most < 1.0 ? 1 : static_cast<int>(most);
+  if (sp > 64) sp = 64;
+  return DecodePlan{sp, used * d * h * elem >= (2 << 20) * static_cast<double>(slots) ? 1 : 0};
 }
 
 hipError_t launch_decode(const DecodeArgs& a, hipStream_t st) {
@@ -676,11 +800,11 @@ hipError_t launch_decode(const DecodeArgs& a, hipStream_t st) {
   else launch_logits<true>(a, st);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  if (a.fmt == kDecodeF32) return launch_phases<Fmt::kF32>(a, st);
-  if (a.fmt == kDecodeBf16) return launch_phases<Fmt::kBf16>(a, st);
-  if (a.W1.gshift == 5) return launch_phases<Fmt::kW4g32>(a, st);
-  if (a.W1.gshift == 6) return launch_phases<Fmt::kW4g64>(a, st);
-  return launch_phases<Fmt::kW4g128>(a, st);
+  if (a.fmt == kDecodeF32) return launch_phases<Fmt::kF32, Fmt::kF32>(a, st);
+  if (a.fmt == kDecodeBf16) return launch_phases<Fmt::kBf16, Fmt::kBf16>(a, st);
+  if (a.W1.gshift == 5) return launch_phases<Fmt::kW4g32, Fmt::kW4g32z>(a, st);
+  if (a.W1.gshift == 6) return launch_phases<Fmt::kW4g64, Fmt::kW4g64z>(a, st);
+  return launch_phases<Fmt::kW4g128, Fmt::kW4g128z>(a, st);
 }
 
 }  // namespace moe

@@ -31,14 +31,18 @@ __device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t voff,
                                                                          static_cast<int>(soff), 0));
 }
 
-// Weight formats; 4-bit codes by their group.
-enum class Fmt { kF32, kBf16, kW4g32, kW4g64, kW4g128 };
+// Weight formats; 4-bit codes by their group, without and with zero points.
+enum class Fmt { kF32, kBf16, kW4g32, kW4g64, kW4g128, kW4g32z, kW4g64z, kW4g128z };
 constexpr bool is_w4(Fmt f) { return f != Fmt::kF32 && f != Fmt::kBf16; }
-// k of one step (all four quarters), of one lane's 16-byte load, and of one MFMA
+constexpr bool has_zeros(Fmt f) { return f == Fmt::kW4g32z || f == Fmt::kW4g64z || f == Fmt::kW4g128z; }
+constexpr int group_shift(Fmt f) {
+  return f == Fmt::kW4g32 || f == Fmt::kW4g32z ? 5 : f == Fmt::kW4g64 || f == Fmt::kW4g64z ? 6 : 7;
+}
+// k of one step (all four quarters) and of one lane's 16-byte load
 constexpr int step_k(Fmt f) { return f == Fmt::kF32 ? 16 : f == Fmt::kBf16 ? 32 : 128; }
 constexpr int lane_k(Fmt f) { return step_k(f) / 4; }
-constexpr int group_shift(Fmt f) { return f == Fmt::kW4g32 ? 5 : f == Fmt::kW4g64 ? 6 : 7; }
-constexpr int acts(Fmt f) { return is_w4(f) ? 4 : 1; }   // 16-byte activation loads per lane and step
+constexpr int acts(Fmt f) { return is_w4(f) ? 4 : 1; }        // 16-byte activation loads per lane and step
+constexpr int act_bytes(Fmt f) { return f == Fmt::kF32 ? 4 : 2; }
 
 // Where a wave finds 16 RT rows of W.  Step s's load of row tile r is at
 // voff[s & 1] + r * tile + (s >> 1) * pair: row-major matrices advance 128 bytes
@@ -52,6 +56,8 @@ struct WRows {
   uint32_t pair, tile;
   __amdgpu_buffer_rsrc_t s, z;   // 4-bit: the rows' scales and zero points
   uint32_t srow, stile;          // 4-bit: first scale of the lane's row, scales of 16 rows
+  bool wide;                     // 4-bit: every four scales from a multiple of four on start at a multiple of
+                                 // four bytes, and so do their zero points
 };
 
 template <Fmt F, int RT>
@@ -73,6 +79,7 @@ __device__ __forceinline__ WRows rows_of(const WMat& m, long long mat, int n0, i
     if (m.z != nullptr) o.z = make_rsrc(m.z + row0 * ng, static_cast<uint32_t>(left) * ng);
     o.srow = static_cast<uint32_t>(r) * ng;
     o.stile = 16u * ng;
+    o.wide = m.wide != 0;
   } else {
     constexpr uint32_t eb = F == Fmt::kF32 ? 4 : 2;
     const uint32_t pitch = static_cast<uint32_t>(m.K) * eb;
@@ -95,6 +102,7 @@ __device__ __forceinline__ WRows rows_of(const WMat& m, long long mat, int n0, i
     }
     o.s = o.z = o.w;
     o.srow = o.stile = 0;
+    o.wide = false;
   }
   return o;
 }
@@ -141,10 +149,10 @@ __device__ __forceinline__ u32x4 to_code_order(u32x4 v) {
 // mfma_k(i) of the step on.
 template <Fmt F>
 __device__ __forceinline__ void arrange_codes(u32x4& v) {
-  if constexpr (F == Fmt::kW4g128) return;
+  if constexpr (group_shift(F) == 7) return;
   auto a = __builtin_amdgcn_permlane32_swap(v.x, v.z, false, false);
   auto b = __builtin_amdgcn_permlane32_swap(v.y, v.w, false, false);
-  if constexpr (F == Fmt::kW4g64) {
+  if constexpr (group_shift(F) == 6) {
     v.x = a[0];
     v.y = b[0];
     v.z = a[1];
@@ -159,153 +167,285 @@ __device__ __forceinline__ void arrange_codes(u32x4& v) {
   }
 }
 template <Fmt F> __device__ __forceinline__ int quarter_k(int q) {
-  if constexpr (F == Fmt::kW4g128) return 32 * q;
-  else if constexpr (F == Fmt::kW4g64) return 32 * (q & 1) + 16 * (q >> 1);
-  else return lane_k(F) < 8 ? 4 * q : 8 * q;   // 4-bit groups of 32, bf16; float32
+  if constexpr (!is_w4(F)) return lane_k(F) * q;
+  else if constexpr (group_shift(F) == 7) return 32 * q;
+  else if constexpr (group_shift(F) == 6) return 32 * (q & 1) + 16 * (q >> 1);
+  else return 8 * q;
 }
 template <Fmt F> constexpr int mfma_k(int i) {
-  return F == Fmt::kW4g128 ? 8 * i : F == Fmt::kW4g64 ? 8 * (i & 1) + 64 * (i >> 1) : 32 * i;
+  return !is_w4(F) ? 0 : group_shift(F) == 7 ? 8 * i : group_shift(F) == 6 ? 8 * (i & 1) + 64 * (i >> 1) : 32 * i;
 }
 
-// Scales of a step: a lane loads the one of its own 32 k; o[g]: that of the
-// step's group g in every lane of the row.
-template <Fmt F>
-__device__ __forceinline__ void spread_scales(uint32_t v, uint32_t (&o)[4]) {
-  o[0] = v;
-  if constexpr (F == Fmt::kW4g128) return;
-  auto h = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-  if constexpr (F == Fmt::kW4g64) {
-    o[0] = h[0];
-    o[1] = h[1];
-  } else {
-    auto a = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
-    auto b = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
-    o[0] = a[0];
-    o[1] = a[1];
-    o[2] = b[0];
-    o[3] = b[1];
+// ---------------------------------------------------------------- a batch --
+// The weights of U steps from step s0 (a multiple of U) on, k < kend.  4-bit:
+// with the batch's scales, two to a word, and zero points, four to a word, in
+// every lane of their row; one load brings as many as it can where the rows
+// allow it (one 2-byte load per step cost 3 to 5 us of a 23 us phase).
+template <Fmt F, int RT, int U> struct WBatch {
+  static constexpr int kS = is_w4(F) ? U << (7 - group_shift(F)) : 2;   // scales of a row and batch
+  static_assert(kS >= 2 && kS <= 16, "whole words of scales");
+  u32x4 w[U][RT];
+  uint32_t sc[RT][kS / 2], zc[RT][(kS + 3) / 4];
+
+  template <int N>
+  static __device__ __forceinline__ void words(uint32_t (&o)[N], __amdgpu_buffer_rsrc_t r, uint32_t off) {
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    if constexpr (N == 1) {
+      o[0] = __builtin_amdgcn_raw_buffer_load_b32(r, static_cast<int>(off), 0, 0);
+    } else if constexpr (N == 2) {
+      const u32x2 v = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(r, static_cast<int>(off), 0, 0));
+      o[0] = v.x;
+      o[1] = v.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) {
+        const u32x4 v = load16(r, off + 4u * i, 0);
+        o[i] = v.x;
+        o[i + 1] = v.y;
+        o[i + 2] = v.z;
+        o[i + 3] = v.w;
+      }
+    }
   }
-}
 
-// ------------------------------------------------------------- streaming --
-// acc[j][r] += A rows of tile j times the 16 rows of W tile r over steps
-// [s0, s1) (of a matrix with K columns), for the first ntile tiles.
-// a: activations; aoff[j] the byte offset of the lane's row (lane % 16) of tile
-// j, or kOut for an empty row.  U steps are loaded together.
+  __device__ __forceinline__ void load(const WRows& wr, int s0, int kend, int q) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int s = s0 + u;
+      const bool in = s * step_k(F) + q * lane_k(F) < kend;
+      const uint32_t vo = s & 1 ? wr.voff[1] : wr.voff[0];
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        w[u][r] = load16(wr.w, in ? vo + r * wr.tile : kOut, static_cast<uint32_t>(s >> 1) * wr.pair);
+    }
+    if constexpr (is_w4(F)) {
+      const uint32_t g0 = static_cast<uint32_t>(s0) << (7 - group_shift(F));
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const uint32_t gi = wr.srow + r * wr.stile + g0;
+        if (wr.wide) {
+          words(sc[r], wr.s, gi * 2u);
+          if constexpr (has_zeros(F)) {
+            if constexpr (kS == 2) zc[r][0] = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(wr.z, static_cast<int>(gi), 0, 0));
+            else words(zc[r], wr.z, gi);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < kS; ++i) {
+            const uint32_t v = static_cast<uint16_t>(
+                __builtin_amdgcn_raw_buffer_load_b16(wr.s, static_cast<int>((gi + i) * 2u), 0, 0));
+            sc[r][i / 2] = i % 2 ? sc[r][i / 2] | (v << 16) : v;
+          }
+          if constexpr (has_zeros(F)) {
+#pragma unroll
+            for (int i = 0; i < kS; ++i) {
+              const uint32_t v = static_cast<uint8_t>(
+                  __builtin_amdgcn_raw_buffer_load_b8(wr.z, static_cast<int>(gi + i), 0, 0));
+              zc[r][i / 4] = i % 4 ? zc[r][i / 4] | (v << (8 * (i % 4))) : v;
+            }
+          }
+        }
+      }
+    }
+  }
+};
+
+// ----------------------------------------------------------------- a step --
+// Products of step u of a batch.  x[j]: the lane's activations of the step for
+// tile j.  live(g): all ones where group g of the step lies below the end of
+// k, else zero (the batch may hold a neighbouring row's scales there).
 // 4-bit: sum (q - z) x over a group is sum (128 + q) x - sum 136 x + (8 - z)
 // sum x.  The products are exact in float32; the middle sum depends on the
 // activations alone, is formed once for all RT tiles and starts the first; the
-// last takes it times -(8 - z) / 136.  kOrdered: the activations are stored in
-// code_order.
-template <Fmt F, int NT, int RT, int U, bool kOrdered, bool kZ>
-__device__ __forceinline__ void stream_rows(floatx4 (&acc)[NT][RT], const WRows& wr,
-                                            __amdgpu_buffer_rsrc_t a, const uint32_t (&arow)[NT], int ntile, int s0,
-                                            int s1, int K, int lane) {
-  constexpr int kK = step_k(F), kA = acts(F);
-  constexpr uint32_t kXe = F == Fmt::kF32 ? 4 : 2;   // bytes of an activation
-  const int q = lane >> 4;
-  const int kend = min(K, s1 * kK);
-  const uint32_t xq = static_cast<uint32_t>(quarter_k<F>(q)) * kXe;
-  uint32_t base = 0;
-  u32x4 neg = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};   // -136
-  if constexpr (is_w4(F)) base = code_base();
-  for (int sb = s0; sb < s1; sb += U) {
-    u32x4 w[U][RT];
-    uint32_t sc[U][RT], zc[U][RT];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int s = sb + u;
-      const bool in = s * kK + q * lane_k(F) < kend;
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        w[u][r] = load16(wr.w, in ? (s & 1 ? wr.voff[1] : wr.voff[0]) + r * wr.tile : kOut,
-                         static_cast<uint32_t>(s >> 1) * wr.pair);
-        if constexpr (is_w4(F)) {
-          const uint32_t gi = wr.srow + r * wr.stile + (static_cast<uint32_t>(s * kK + q * 32) >> group_shift(F));
-          sc[u][r] = static_cast<uint16_t>(
-              __builtin_amdgcn_raw_buffer_load_b16(wr.s, static_cast<int>(in ? gi * 2u : kOut), 0, 0));
-          if constexpr (kZ)
-            zc[u][r] = static_cast<uint8_t>(
-                __builtin_amdgcn_raw_buffer_load_b8(wr.z, static_cast<int>(in ? gi : kOut), 0, 0));
-        }
-      }
-    }
+// last takes it times -(8 - z) / 136.
+template <Fmt F, int NT, int RT, int U, typename Live>
+__device__ __forceinline__ void multiply_step(floatx4 (&acc)[NT][RT], const WBatch<F, RT, U>& b, int u,
+                                              const u32x4 (&x)[NT][acts(F)], Live live) {
+  if constexpr (F == Fmt::kF32) {
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      if (NT > 1 && j >= ntile) break;
-      if constexpr (NT > 1) __builtin_amdgcn_sched_barrier(0);   // one tile's activations at a time: registers
-      u32x4 x[U][kA];
+      const floatx4 xv = __builtin_bit_cast(floatx4, x[j][0]);
 #pragma unroll
-      for (int u = 0; u < U; ++u)
+      for (int r = 0; r < RT; ++r) {
+        const floatx4 wv = __builtin_bit_cast(floatx4, b.w[u][r]);
 #pragma unroll
-        for (int g = 0; g < kA; ++g) {
-          const int k0 = (sb + u) * kK + (is_w4(F) ? mfma_k<F>(g) : 0);
-          const bool in = is_w4(F) ? k0 < kend : k0 + q * lane_k(F) < kend;
-          x[u][g] = load16(a, in ? arow[j] + xq : kOut, static_cast<uint32_t>(k0) * kXe);
-        }
+        for (int i = 0; i < 4; ++i) acc[j][r] = __builtin_amdgcn_mfma_f32_16x16x4f32(xv[i], wv[i], acc[j][r], 0, 0, 0);
+      }
+    }
+  } else if constexpr (F == Fmt::kBf16) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if constexpr (F == Fmt::kF32) {
-          const floatx4 xv = __builtin_bit_cast(floatx4, x[u][0]);
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            const floatx4 wv = __builtin_bit_cast(floatx4, w[u][r]);
+      for (int r = 0; r < RT; ++r)
+        acc[j][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[j][0]),
+                                                            __builtin_bit_cast(bf16x8, b.w[u][r]), acc[j][r], 0, 0, 0);
+  } else {
+    constexpr int kG = 128 >> group_shift(F), kPer = 4 / kG;   // groups of a step, MFMAs of a group
+    const uint32_t base = code_base();
+    const u32x4 neg = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};   // -136
+    floatx4 n136[NT][kG];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[j][r] = __builtin_amdgcn_mfma_f32_16x16x4f32(xv[i], wv[i], acc[j][r], 0, 0, 0);
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int g = 0; g < kG; ++g) {
+        n136[j][g] = floatx4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          n136[j][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[j][g * kPer + i]),
+                                                               __builtin_bit_cast(bf16x8, neg), n136[j][g], 0, 0, 0);
+      }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      u32x4 c = b.w[u][r];
+      arrange_codes<F>(c);
+#pragma unroll
+      for (int g = 0; g < kG; ++g) {
+        const int si = u * kG + g;
+        bf16x8 cv[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) cv[i] = codes_to_bf16(c[g * kPer + i], base);
+        const uint32_t sw = si % 2 ? b.sc[r][si / 2] & 0xffff0000u : b.sc[r][si / 2] << 16;
+        const float s = __uint_as_float(sw & live(g));
+        float zf = 0.f;
+        if constexpr (has_zeros(F))
+          zf = static_cast<float>((b.zc[r][si / 4] >> (8 * (si % 4))) & 15u) * (1.f / 136.f) - 8.f / 136.f;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          floatx4 t = n136[j][g];
+#pragma unroll
+          for (int i = 0; i < kPer; ++i)
+            t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[j][g * kPer + i]), cv[i], t, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if constexpr (has_zeros(F)) t[i] = fmaf(zf, n136[j][g][i], t[i]);
+            acc[j][r][i] = fmaf(s, t[i], acc[j][r][i]);
           }
-        } else if constexpr (F == Fmt::kBf16) {
-#pragma unroll
-          for (int r = 0; r < RT; ++r)
-            acc[j][r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[u][0]),
-                                                                __builtin_bit_cast(bf16x8, w[u][r]), acc[j][r], 0, 0, 0);
-        } else {
-          __builtin_amdgcn_sched_barrier(0);
-          constexpr int kG = 128 >> group_shift(F), kPer = 4 / kG;   // groups of a step, MFMAs of a group
-          floatx4 n136[kG];
-#pragma unroll
-          for (int g = 0; g < kG; ++g) {
-            n136[g] = floatx4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < kPer; ++i) {
-              u32x4& xv = x[u][g * kPer + i];
-              if constexpr (!kOrdered) xv = to_code_order(xv);
-              n136[g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xv),
-                                                                __builtin_bit_cast(bf16x8, neg), n136[g], 0, 0, 0);
-            }
-          }
-#pragma unroll
-          for (int r = 0; r < RT; ++r) {
-            if constexpr (RT > 1) __builtin_amdgcn_sched_barrier(0);
-            u32x4 c = w[u][r];
-            // with several tiles the codes are unpacked anew for each: kept
-            // unpacked they would take four times the registers
-            uint32_t sv = sc[u][r];
-            if constexpr (NT > 1) __asm__ volatile("" : "+v"(c.x), "+v"(c.y), "+v"(c.z), "+v"(c.w), "+v"(sv));
-            arrange_codes<F>(c);
-            uint32_t sg[4], zg[4];
-            spread_scales<F>(sv, sg);
-            if constexpr (kZ) spread_scales<F>(zc[u][r], zg);
-#pragma unroll
-            for (int g = 0; g < kG; ++g) {
-              floatx4 t = n136[g];
-#pragma unroll
-              for (int i = 0; i < kPer; ++i)
-                t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[u][g * kPer + i]),
-                                                            codes_to_bf16(c[g * kPer + i], base), t, 0, 0, 0);
-              const float s = __uint_as_float(sg[g] << 16);
-              if constexpr (kZ) {
-                const float zf = static_cast<float>(zg[g] & 15u) * (1.f / 136.f) - 8.f / 136.f;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) t[i] = fmaf(zf, n136[g][i], t[i]);
-              }
-#pragma unroll
-              for (int i = 0; i < 4; ++i) acc[j][r][i] = fmaf(s, t[i], acc[j][r][i]);
-            }
-          }
+          // the sums stay here: moved behind the loop's branches, they would
+          // keep every group's products in registers until then
+          __asm__ volatile("" : "+v"(acc[j][r]));
         }
       }
     }
   }
 }
+
+// -------------------------------------------------------------- a segment --
+// A wave's share of a product: W rows (WRows), steps [s0, s1) of them (s0 a
+// multiple of U), and `slots` rows of activations.
+//
+// The activations go through LDS of the wave's own (no barriers).  Most rows of
+// an operand are empty when an expert has one or two tokens: read for every step
+// by the lanes that need them, the few rows would take as many load instructions
+// as the weights; staged, a row's bytes are read once, densely.  Slot i of the
+// region holds a chunk of steps of row i, padded by 16 bytes so that neighbouring
+// rows start in different banks; the region's last 16 bytes are zero.
+//
+// begin() issues the first loads, run() does the rest: called before the work
+// that ends the segment before (sums across waves, activation, stores), begin()
+// keeps the memory busy meanwhile.
+constexpr int kStageZero = 16;
+
+template <Fmt F, int RT, int U, bool kOrdered, int SLOTS, int STAGE> struct Stream {
+  static constexpr int kStep = step_k(F) * act_bytes(F);     // activation bytes of a step and row
+  static constexpr int kLoads = (STAGE - kStageZero + 1023) / 1024;
+  static constexpr bool kDense = SLOTS * (U * kStep + 16) + kStageZero > STAGE;   // a chunk may be shorter than a batch
+  static_assert(STAGE % 16 == 0 && STAGE >= SLOTS * (kStep + 16) + kStageZero, "one step of all rows fits");
+
+  WRows wr;
+  WBatch<F, RT, U> w;
+  u32x4 xv[kLoads];
+  int s0, s1, kend, slots, cs;
+
+  static __device__ __forceinline__ void clear(char* stage, int lane) {
+    if (lane < kStageZero / 4) reinterpret_cast<int*>(stage + STAGE - kStageZero)[lane] = 0;
+  }
+
+  // the chunk of activations from step c0 on: slot i at soff(i) bytes of a
+  template <typename SlotOff>
+  __device__ __forceinline__ void load_x(__amdgpu_buffer_rsrc_t a, SlotOff soff, int c0, int lane) {
+    constexpr int kUnits = kStep == 64 ? 2 : 4;              // log2 of a step's 16-byte units
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int unit = i * 64 + lane, slot = unit >> (cs + kUnits);
+      const int at = c0 * kStep + ((unit & ((1 << (cs + kUnits)) - 1)) << 4);
+      xv[i] = load16(a, slot < slots && at < kend * act_bytes(F) ? soff(slot) + at : kOut, 0);
+    }
+  }
+  __device__ __forceinline__ void store_x(char* stage, int lane) {
+    constexpr int kUnits = kStep == 64 ? 2 : 4;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int unit = i * 64 + lane, slot = unit >> (cs + kUnits);
+      if (slot < slots)
+        *reinterpret_cast<u32x4*>(stage + slot * ((kStep << cs) + 16) + ((unit & ((1 << (cs + kUnits)) - 1)) << 4)) = xv[i];
+    }
+  }
+
+  template <typename SlotOff>
+  __device__ __forceinline__ void begin(const WRows& rows, __amdgpu_buffer_rsrc_t a, SlotOff soff, int nslots, int first,
+                                        int last, int K, int lane) {
+    wr = rows;
+    slots = nslots;
+    s0 = first;
+    s1 = last;
+    kend = min(K, s1 * step_k(F));
+    cs = 0;   // log2 of a chunk's steps: as many as fit
+    while (slots * ((kStep << (cs + 1)) + 16) <= STAGE - kStageZero && cs < 10) ++cs;
+    if (s0 >= s1) return;
+    load_x(a, soff, s0, lane);
+    w.load(wr, s0, kend, lane >> 4);
+  }
+
+  // acc[j][r] += rows of tile j times the 16 rows of W tile r; rslot[j]: slot of
+  // the lane's row (lane % 16) of tile j (any, if the row is empty: its sums are
+  // not read)
+  template <int NT, typename SlotOff>
+  __device__ __forceinline__ void run(floatx4 (&acc)[NT][RT], __amdgpu_buffer_rsrc_t a, SlotOff soff,
+                                      const int (&rslot)[NT], char* stage, int lane) {
+    if (s0 < s1) {
+      const int q = lane >> 4, steps = 1 << cs;
+      const char* zero = stage + STAGE - kStageZero;
+      const char* xrow[NT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        xrow[j] = stage + rslot[j] * ((kStep << cs) + 16) + quarter_k<F>(q) * act_bytes(F);
+      store_x(stage, lane);
+      int cb = s0;
+      for (int s = s0;;) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if ((u == 0 || kDense) && s + u >= cb + steps && s + u < s1) {
+            cb = s + u;
+            load_x(a, soff, cb, lane);
+            store_x(stage, lane);
+          }
+          u32x4 x[NT][acts(F)];
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int g = 0; g < acts(F); ++g) {
+              const char* at = xrow[j] + (s + u - cb) * kStep + mfma_k<F>(g) * act_bytes(F);
+              x[j][g] = *reinterpret_cast<const u32x4*>(s + u < s1 ? at : zero);
+              if constexpr (is_w4(F) && !kOrdered) x[j][g] = to_code_order(x[j][g]);
+            }
+          multiply_step<F, NT, RT, U>(acc, w, u, x, [&](int g) {
+            return (s + u) * step_k(F) + (g << group_shift(F)) < kend ? 0xffffffffu : 0u;
+          });
+        }
+        s += U;
+        if (s >= s1) break;
+        w.load(wr, s, kend, q);
+      }
+    }
+    // Wait states between the last products and whatever reads them, placed by
+    // hand: where a uniform branch separated an MFMA from its reader, hipcc has
+    // been seen to leave them out on the taken side.  For the same reason no
+    // branch depends on the number of tiles between products.
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) __asm__ volatile("s_nop 15" : "+v"(acc[j][r]));
+  }
+};
 
 }  // namespace moe

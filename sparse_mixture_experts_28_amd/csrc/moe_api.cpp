@@ -300,6 +300,11 @@ namespace {
 
 int group_shift(int32_t group) { return group == 32 ? 5 : group == 64 ? 6 : group == 128 ? 7 : -1; }
 
+WMat w4_matrix(const uint8_t* codes, const void* scales, const uint8_t* zeros, int N, int K, int gs) {
+  const int wide = ((K >> gs) % 4 == 0 && aligned(scales, 4) && (zeros == nullptr || aligned(zeros, 4))) ? 1 : 0;
+  return WMat{reinterpret_cast<const char*>(codes), static_cast<const uint16_t*>(scales), zeros, N, K, 0, gs, wide};
+}
+
 // The few-row kernels address the activations, the hidden rows and 16 weight
 // rows through buffer ranges below 2^31 bytes.
 moe_status_t check_shape_decode(int32_t T, int32_t d, int32_t h, int32_t E, int32_t k, int32_t S, int dtype) {
@@ -313,18 +318,19 @@ moe_status_t check_shape_decode(int32_t T, int32_t d, int32_t h, int32_t E, int3
 
 struct DecodeLayout {
   size_t logits, xord, hid, part, counters, total;
-  int split, ncounter;
+  DecodePlan plan;
+  int ncounter;
 };
 
 DecodeLayout decode_layout(int32_t T, int32_t d, int32_t h, int32_t E, int32_t k, int32_t S, int fmt) {
   DecodeLayout L;
-  L.split = decode_split(T, d, h, E, k, S, fmt);
-  L.ncounter = (d + 15) / 16;
+  L.plan = decode_plan(T, d, h, E, k, S, fmt);
+  L.ncounter = 2 + (d + 15) / 16;   // items handed out in phase 1 and 2, arrivals per column tile
   size_t off = 0;
   L.logits = off;   off += align_up(static_cast<size_t>(T) * E * 8);
   L.xord = off;     off += align_up(fmt == kDecodeW4 ? static_cast<size_t>(T) * d * 2 : 0);
   L.hid = off;      off += align_up(static_cast<size_t>(T) * (k + S) * h * 4);
-  L.part = off;     off += align_up(L.split > 1 ? static_cast<size_t>(L.split) * T * d * 4 : 0);
+  L.part = off;     off += align_up(L.plan.split > 1 ? static_cast<size_t>(L.plan.split) * T * d * 4 : 0);
   L.counters = off; off += align_up(static_cast<size_t>(L.ncounter) * 4);
   L.total = off;
   return L;
@@ -360,7 +366,8 @@ moe_status_t forward_decode(DecodeArgs a, const moe_launch_t* launch) {
   a.part = reinterpret_cast<float*>(b + L.part);
   a.counters = reinterpret_cast<int32_t*>(b + L.counters);
   a.ncounter = L.ncounter;
-  a.split = L.split;
+  a.split = L.plan.split;
+  a.dynamic = L.plan.dynamic;
   (void)hipGetLastError();
   const hipError_t e = launch_decode(a, launch->stream);
   if (e != hipSuccess) {
@@ -560,8 +567,8 @@ moe_status_t moe_forward_decode(const void* x, const void* W_g, const void* W1, 
   a.x = x; a.W_g = W_g; a.b1 = b1; a.b2 = b2; a.out = out; a.topk_idx = topk_idx; a.topk_w = topk_w;
   a.E = E; a.k = k; a.S = n_shared;
   a.fmt = launch->dtype == MOE_BF16 ? kDecodeBf16 : kDecodeF32;
-  a.W1 = WMat{static_cast<const char*>(W1), nullptr, nullptr, h, d, launch->weights_packed, 0};
-  a.W2 = WMat{static_cast<const char*>(W2), nullptr, nullptr, d, h, launch->weights_packed, 0};
+  a.W1 = WMat{static_cast<const char*>(W1), nullptr, nullptr, h, d, launch->weights_packed, 0, 0};
+  a.W2 = WMat{static_cast<const char*>(W2), nullptr, nullptr, d, h, launch->weights_packed, 0, 0};
   return forward_decode(a, launch);
 }
 
@@ -585,8 +592,8 @@ moe_status_t moe_forward_decode_w4(const void* x, const void* W_g, const uint8_t
   a.x = x; a.W_g = W_g; a.b1 = b1; a.b2 = b2; a.out = out; a.topk_idx = topk_idx; a.topk_w = topk_w;
   a.E = E; a.k = k; a.S = n_shared;
   a.fmt = kDecodeW4;
-  a.W1 = WMat{reinterpret_cast<const char*>(W1), static_cast<const uint16_t*>(W1_scales), W1_zeros, h, d, 0, gs};
-  a.W2 = WMat{reinterpret_cast<const char*>(W2), static_cast<const uint16_t*>(W2_scales), W2_zeros, d, h, 0, gs};
+  a.W1 = w4_matrix(W1, W1_scales, W1_zeros, h, d, gs);
+  a.W2 = w4_matrix(W2, W2_scales, W2_zeros, d, h, gs);
   return forward_decode(a, launch);
 }
 
@@ -626,9 +633,8 @@ moe_status_t moe_linear_w4(const void* x, int32_t M, const uint8_t* codes, const
   if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 2) || !aligned(y, 2) || (bias && !aligned(bias, 2)))
     return MOE_ERR_UNSUPPORTED;
   (void)hipGetLastError();
-  return w4_status(launch_w4_linear(static_cast<const uint16_t*>(x), M, codes, static_cast<const uint16_t*>(scales),
-                                    zeros, N, K, gs, static_cast<const uint16_t*>(bias), static_cast<uint16_t*>(y),
-                                    stream),
+  return w4_status(launch_w4_linear(static_cast<const uint16_t*>(x), M, w4_matrix(codes, scales, zeros, N, K, gs),
+                                    static_cast<const uint16_t*>(bias), static_cast<uint16_t*>(y), stream),
                    "4-bit Linear");
 }
 

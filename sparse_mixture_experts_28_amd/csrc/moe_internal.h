@@ -328,6 +328,7 @@ struct WMat {
   int N, K;
   int packed;          // bf16: tile-packed layout
   int gshift;          // 4-bit: log2 of the elements per scale
+  int wide;            // 4-bit: K / group a multiple of four, scales and zero points 4-byte aligned
 };
 enum DecodeFmt { kDecodeF32 = 0, kDecodeBf16 = 1, kDecodeW4 = 2 };
 struct DecodeArgs {
@@ -350,16 +351,19 @@ struct DecodeArgs {
   int T, d, h, E, k, S;
   int act;
   int fmt;
-  int split;            // shares of phase 2's sum per 16 output columns
+  int split;            // shares of phase 2's sum per tile of output columns
+  int dynamic;          // items handed out by a counter
 };
-int decode_split(int T, int d, int h, int E, int k, int S, int fmt);
+struct DecodePlan {
+  int split, dynamic;
+};
+DecodePlan decode_plan(int T, int d, int h, int E, int k, int S, int fmt);
 hipError_t launch_decode(const DecodeArgs& a, hipStream_t st);
 hipError_t launch_w4_quantize(const uint16_t* src, long long n, int gshift, uint8_t* codes, uint16_t* scales,
                               uint8_t* zeros, hipStream_t st);
 hipError_t launch_w4_dequantize(const uint8_t* codes, const uint16_t* scales, const uint8_t* zeros, long long n,
                                 int gshift, uint16_t* dst, hipStream_t st);
-hipError_t launch_w4_linear(const uint16_t* x, int M, const uint8_t* codes, const uint16_t* scales,
-                            const uint8_t* zeros, int N, int K, int gshift, const uint16_t* bias, uint16_t* y,
+hipError_t launch_w4_linear(const uint16_t* x, int M, const WMat& w, const uint16_t* bias, uint16_t* y,
                             hipStream_t st);
 
 // the top-k layer on a given workspace (moe_api.cpp)

@@ -94,31 +94,38 @@ __global__ __launch_bounds__(256) void w4_dequantize_kernel(const uint32_t* code
 // ------------------------------------------------------------------ Linear --
 // y[m, n] = sum_k x[m, k] w[n, k] + b[n].  One workgroup per 16 columns and 64
 // rows; its waves split k and add their sums in LDS in wave order.
-template <Fmt F, int NT, int RT, int U, int NW>
+template <Fmt F, int NT, int RT, int U, int NW, int STAGE>
 __global__ __launch_bounds__(NW * 64) void w4_linear_kernel(const uint16_t* x, WMat w, const uint16_t* bias,
                                                             uint16_t* y, int M) {
-  __shared__ float red[NT * RT * NW * 256];
+  // the waves' activation regions, then their sums
+  constexpr int kSums = NT * RT * NW * 1024;
+  __shared__ __attribute__((aligned(16))) char lds[NW * STAGE > kSums ? NW * STAGE : kSums];
+  float* red = reinterpret_cast<float*>(lds);
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int n0 = blockIdx.x * 16 * RT, m0 = blockIdx.y * 64;
   const int rows = min(M - m0, 64);
   const uint32_t pitch = static_cast<uint32_t>(w.K) * 2u;
   const __amdgpu_buffer_rsrc_t xr =
       make_rsrc(x + static_cast<size_t>(m0) * w.K, static_cast<uint32_t>(rows) * pitch);
-  uint32_t arow[NT];
+  char* mine = lds + wave * STAGE;
+  using St = Stream<F, RT, U, false, 16 * NT, STAGE>;
+  St::clear(mine, lane);
+  int rslot[NT];
   floatx4 acc[NT][RT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    const int p = j * 16 + (lane & 15);
-    arow[j] = p < rows ? static_cast<uint32_t>(p) * pitch : kOut;
+    rslot[j] = min(j * 16 + (lane & 15), rows - 1);
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[j][r] = floatx4{0.f, 0.f, 0.f, 0.f};
   }
   const int tl = (rows + 15) / 16;
-  const int nst = (w.K + 127) / 128;
-  const int s0 = wave * nst / NW, s1 = (wave + 1) * nst / NW;
-  const WRows wr = rows_of<F, RT>(w, 0, n0, lane);
-  if (w.z != nullptr) stream_rows<F, NT, RT, U, false, true>(acc, wr, xr, arow, tl, s0, s1, w.K, lane);
-  else stream_rows<F, NT, RT, U, false, false>(acc, wr, xr, arow, tl, s0, s1, w.K, lane);
+  const int nst = (w.K + 127) / 128, nb = (nst + U - 1) / U;
+  const int s0 = wave * nb / NW * U, s1 = min(nst, (wave + 1) * nb / NW * U);
+  auto soff = [&](int slot) { return static_cast<uint32_t>(slot) * pitch; };
+  St st;
+  st.begin(rows_of<F, RT>(w, 0, n0, lane), xr, soff, rows, s0, s1, w.K, lane);
+  st.run(acc, xr, soff, rslot, mine, lane);
+  __syncthreads();
 #pragma unroll
   for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -151,13 +158,17 @@ __global__ __launch_bounds__(NW * 64) void w4_linear_kernel(const uint16_t* x, W
 #define LRT4 2
 #endif
 #ifndef LU4
-#define LU4 1
+#define LU4 2
 #endif
 template <Fmt F>
 hipError_t launch_linear(const uint16_t* x, int M, const WMat& w, const uint16_t* bias, uint16_t* y, hipStream_t st) {
   const unsigned gy = (M + 63) / 64;
-  if (M <= 16) w4_linear_kernel<F, 1, LRT, LU, LNW><<<dim3((w.N + 16 * LRT - 1) / (16 * LRT), gy), LNW * 64, 0, st>>>(x, w, bias, y, M);
-  else w4_linear_kernel<F, 4, LRT4, LU4, 8><<<dim3((w.N + 16 * LRT4 - 1) / (16 * LRT4), gy), 512, 0, st>>>(x, w, bias, y, M);
+  if (M <= 16)
+    w4_linear_kernel<F, 1, LRT, LU, LNW, 4864>
+        <<<dim3((w.N + 16 * LRT - 1) / (16 * LRT), gy), LNW * 64, 0, st>>>(x, w, bias, y, M);
+  else
+    w4_linear_kernel<F, 4, LRT4, LU4, 8, 17424>
+        <<<dim3((w.N + 16 * LRT4 - 1) / (16 * LRT4), gy), 512, 0, st>>>(x, w, bias, y, M);
   return hipGetLastError();
 }
 
@@ -183,13 +194,13 @@ hipError_t launch_w4_dequantize(const uint8_t* codes, const uint16_t* scales, co
   return hipGetLastError();
 }
 
-hipError_t launch_w4_linear(const uint16_t* x, int M, const uint8_t* codes, const uint16_t* scales,
-                            const uint8_t* zeros, int N, int K, int gshift, const uint16_t* bias, uint16_t* y,
+hipError_t launch_w4_linear(const uint16_t* x, int M, const WMat& w, const uint16_t* bias, uint16_t* y,
                             hipStream_t st) {
-  const WMat w{reinterpret_cast<const char*>(codes), scales, zeros, N, K, 0, gshift};
-  if (gshift == 5) return launch_linear<Fmt::kW4g32>(x, M, w, bias, y, st);
-  if (gshift == 6) return launch_linear<Fmt::kW4g64>(x, M, w, bias, y, st);
-  return launch_linear<Fmt::kW4g128>(x, M, w, bias, y, st);
+  if (w.gshift == 5)
+    return w.z ? launch_linear<Fmt::kW4g32z>(x, M, w, bias, y, st) : launch_linear<Fmt::kW4g32>(x, M, w, bias, y, st);
+  if (w.gshift == 6)
+    return w.z ? launch_linear<Fmt::kW4g64z>(x, M, w, bias, y, st) : launch_linear<Fmt::kW4g64>(x, M, w, bias, y, st);
+  return w.z ? launch_linear<Fmt::kW4g128z>(x, M, w, bias, y, st) : launch_linear<Fmt::kW4g128>(x, M, w, bias, y, st);
 }
 
 }  // namespace moe
