@@ -9,10 +9,11 @@ passes torch's current stream.  Nothing here computes any part of the layer.
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 from typing import Optional, Sequence
 
-from ._lib import (EXPORTS, LIB_PATH, MOE_ACT_GELU, MOE_ACT_SILU, MOE_BF16, MOE_ERR_ARG, MOE_ERR_HIP,
+from ._lib import (EXPORTS, LIB, LIB_PATH, MOE_ACT_GELU, MOE_ACT_SILU, MOE_BF16, MOE_ERR_ARG, MOE_ERR_HIP,
                    MOE_ERR_SCRATCH, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_F32, MOE_MAX_EXPERTS, MOE_MAX_SHARED,
                    MOE_MAX_TOPK, MOE_NOALLOC_SCRATCH_BYTES, MOE_NUM_STAGE_EVENTS, MOE_OK, MoeLaunch,
                    moe_expert_choice_capacity, moe_forward, moe_forward_expert_choice, moe_forward_noalloc,
@@ -305,6 +306,8 @@ def forward_mxfp8(x, W_g, W1, W1s, b1, W2, W2s, b2, k: int, capacity_factor: flo
 
 
 # ------------------------------------------------------ few-token operators --
+# A generation step makes many of these calls and waits for each, so their host
+# side is kept short: about 7 us a call beyond the launches themselves.
 
 @dataclass
 class DecodeOutput:
@@ -313,45 +316,76 @@ class DecodeOutput:
     topk_w: "object"         # [T, k] float32
 
 
-def _on_device(dev):
-    """The device as the current one for the launches of a call (they go to its current stream)."""
-    import contextlib
+_decode_bytes = functools.lru_cache(maxsize=None)(moe_workspace_bytes_decode)
+_decode_bytes_w4 = functools.lru_cache(maxsize=None)(moe_workspace_bytes_decode_w4)
+
+
+def _on(t, gpu: int, dtype) -> bool:
+    """t is a contiguous tensor of that dtype on that GPU."""
+    return t.dtype is dtype and t.get_device() == gpu and t.is_contiguous()
+
+
+def _gpu_of(t) -> int:
+    """The tensor's GPU, or -1."""
+    return t.get_device()
+
+
+def _call(gpu: int, fn, *args) -> None:
+    """fn(*args, stream) on the GPU's current stream, with that GPU current (launches go to the current device)."""
     import torch
-    return contextlib.nullcontext() if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-
-
-def _decode_outputs(x, k, nbytes, workspace):
-    """Outputs and workspace of a few-token call; a workspace that is given has to be large enough."""
-    import torch
-    T, d = x.shape
-    if nbytes == 0:
-        raise RuntimeError("unsupported problem shape for the few-token layer")
-    if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=x.device)
-    elif workspace.device != x.device or not workspace.is_contiguous() or \
-            workspace.numel() * workspace.element_size() < nbytes:
-        raise ValueError(f"workspace must be a contiguous tensor of at least {nbytes} bytes on the same GPU")
-    return (torch.empty((T, d), dtype=x.dtype, device=x.device),
-            torch.empty((T, k), dtype=torch.int32, device=x.device),
-            torch.empty((T, k), dtype=torch.float32, device=x.device), workspace)
-
-
-def _decode_launch(x, h, dt, b_g, b_sel, activation, workspace):
-    import torch
-    launch = MoeLaunch()
-    launch.T, launch.d = x.shape
-    launch.h, launch.dtype = h, dt
-    launch.b_g = b_g.data_ptr() if b_g is not None else None
-    launch.b_sel = b_sel.data_ptr() if b_sel is not None else None
-    launch.workspace = workspace.data_ptr()
-    launch.workspace_bytes = workspace.numel() * workspace.element_size()
-    launch.stream = torch.cuda.current_stream(x.device).cuda_stream
-    launch.activation = ACTIVATIONS[activation]
-    return launch
+    if torch.cuda.current_device() == gpu:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(gpu))
+    else:
+        with torch.cuda.device(gpu):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(gpu))
+    if status != MOE_OK:
+        raise RuntimeError(moe_status_string(status))
 
 
 def _ptr(t):
-    return t.data_ptr() if t is not None else None
+    return None if t is None else t.data_ptr()
+
+
+def _decode(fn, x, W_g, weights, b1, W1, b2, k, S, b_g, b_sel, activation, packed, workspace, nbytes, extra=()):
+    """Checks shared by the few-token layers, outputs, workspace and the call.
+    ``weights``: the weight arguments in the order of the C call; ``extra``:
+    what stands between them and E."""
+    import torch
+    gpu = _gpu_of(x)
+    T, d = x.shape
+    E, h = W_g.shape[0], W1.shape[1]
+    dt = x.dtype
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
+    if gpu < 0 or not x.is_contiguous() or not _on(W_g, gpu, dt) or (b1 is not None and not _on(b1, gpu, dt)) or \
+            (b2 is not None and not _on(b2, gpu, dt)):
+        raise ValueError("x, W_g and the biases must be contiguous tensors of one dtype on one GPU")
+    if W_g.shape != (E, d) or (b1 is not None and b1.shape != (E + S, h)) or \
+            (b2 is not None and b2.shape != (E + S, d)):
+        raise ValueError("inconsistent shapes")
+    for name, b in (("b_g", b_g), ("b_sel", b_sel)):
+        if b is not None and (not _on(b, gpu, torch.float32) or b.shape != (E,)):
+            raise ValueError(f"{name} must be a contiguous float32 [E] on the same GPU")
+    if nbytes == 0:
+        raise RuntimeError("unsupported problem shape for the few-token layer")
+    dev = x.device
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    elif workspace.get_device() != gpu or not workspace.is_contiguous() or \
+            workspace.numel() * workspace.element_size() < nbytes:
+        raise ValueError(f"workspace must be a contiguous tensor of at least {nbytes} bytes on the same GPU")
+    out = torch.empty((T, d), dtype=dt, device=dev)
+    topk_idx = torch.empty((T, k), dtype=torch.int32, device=dev)
+    topk_w = torch.empty((T, k), dtype=torch.float32, device=dev)
+
+    def call(stream):
+        launch = MoeLaunch(T=T, d=d, h=h, dtype=MOE_BF16 if dt is torch.bfloat16 else MOE_F32, b_g=_ptr(b_g),
+                           workspace=workspace.data_ptr(), workspace_bytes=nbytes, stream=stream,
+                           activation=ACTIVATIONS[activation], b_sel=_ptr(b_sel), weights_packed=packed)
+        return fn(x.data_ptr(), W_g.data_ptr(), *weights, *extra, E, k, S, out.data_ptr(), topk_idx.data_ptr(),
+                  topk_w.data_ptr(), ctypes.byref(launch))
+    _call(gpu, call)
+    return DecodeOutput(out, topk_idx, topk_w)
 
 
 def forward_decode(x, W_g, W1, b1, W2, b2, k: int, n_shared: int = 0, b_g=None, *, activation: str = "gelu",
@@ -360,34 +394,31 @@ def forward_decode(x, W_g, W1, b1, W2, b2, k: int, n_shared: int = 0, b_g=None, 
     the same layer without a capacity limit and without the losses, made for
     reading the taken experts' weights once.
 
-    Tensors as for ``forward``.  ``workspace``: a uint8 tensor of at least
+    Tensors as for ``forward``.  ``workspace``: a tensor of at least
     ``moe_workspace_bytes_decode(T, d, h, E, k, n_shared, dtype)`` bytes, or
     None (allocated).  Calls that may overlap, graph replays among them, need
     workspaces of their own."""
-    _check_tensors(x, W_g, W1, b1, W2, b2, b_g, n_shared, activation)
-    E, h = W_g.shape[0], W1.shape[1]
-    _check_b_sel(b_sel, E, x.device)
     dt = _dtype_code(x)
-    nbytes = moe_workspace_bytes_decode(x.shape[0], x.shape[1], h, E, k, n_shared, dt)
-    out, topk_idx, topk_w, workspace = _decode_outputs(x, k, nbytes, workspace)
-    launch = _decode_launch(x, h, dt, b_g, b_sel, activation, workspace)
-    launch.weights_packed = 1 if weights_packed else 0
-    with _on_device(x.device):
-        status = moe_forward_decode(x.data_ptr(), W_g.data_ptr(), W1.data_ptr(), _ptr(b1), W2.data_ptr(), _ptr(b2), E,
-                                    k, n_shared, out.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(), launch)
-    if status != MOE_OK:
-        raise RuntimeError(moe_status_string(status))
-    return DecodeOutput(out, topk_idx, topk_w)
+    gpu = _gpu_of(x)
+    T, d = x.shape
+    E, h, S = W_g.shape[0], W1.shape[1], n_shared
+    if not _on(W1, gpu, x.dtype) or not _on(W2, gpu, x.dtype):
+        raise ValueError("W1 and W2 must be contiguous tensors of x's dtype on its GPU")
+    if W1.shape != (E + S, h, d) or W2.shape != (E + S, d, h):
+        raise ValueError("inconsistent shapes")
+    return _decode(LIB.moe_forward_decode, x, W_g, (W1.data_ptr(), _ptr(b1), W2.data_ptr(), _ptr(b2)), b1, W1, b2, k, S,
+                   b_g, b_sel, activation, 1 if weights_packed else 0, workspace, _decode_bytes(T, d, h, E, k, S, dt))
 
 
-def _w4_group(codes, scales, zeros, dev) -> int:
+def _w4_group(codes, scales, zeros, gpu: int) -> int:
     """Checks one 4-bit tensor (codes [..., K/2], scales and zeros [..., K/group]); returns the group."""
     import torch
-    for t, dt in ((codes, torch.uint8), (scales, torch.bfloat16), (zeros, torch.uint8)):
-        if t is not None and (not t.is_cuda or t.device != dev or not t.is_contiguous() or t.dtype != dt):
-            raise ValueError("4-bit weights are contiguous uint8 codes, bfloat16 scales and uint8 zeros on one GPU")
-    K, ng = 2 * codes.shape[-1], scales.shape[-1]
-    if scales.shape[:-1] != codes.shape[:-1] or (zeros is not None and zeros.shape != scales.shape) or ng < 1 or K % ng:
+    if gpu < 0 or not _on(codes, gpu, torch.uint8) or not _on(scales, gpu, torch.bfloat16) or \
+            (zeros is not None and not _on(zeros, gpu, torch.uint8)):
+        raise ValueError("4-bit weights are contiguous uint8 codes, bfloat16 scales and uint8 zeros on one GPU")
+    cs, ss = codes.shape, scales.shape
+    K, ng = 2 * cs[-1], ss[-1]
+    if ss[:-1] != cs[:-1] or (zeros is not None and zeros.shape != ss) or ng < 1 or K % ng:
         raise ValueError("inconsistent shapes of 4-bit codes, scales and zeros")
     group = K // ng
     if group not in (32, 64, 128):
@@ -401,19 +432,18 @@ def quantize_w4(w, group: int = 128, zero_points: bool = False):
     bfloat16 [..., K/group], zeros uint8 [..., K/group], or None for the
     symmetric form).  The rule is ``moe_quantize_w4``'s."""
     import torch
-    if w.dtype != torch.bfloat16 or not w.is_cuda or not w.is_contiguous() or w.dim() < 1 or w.numel() == 0:
+    gpu = _gpu_of(w)
+    if gpu < 0 or not _on(w, gpu, torch.bfloat16) or w.dim() < 1 or w.numel() == 0:
         raise ValueError("quantize_w4 takes a contiguous, non-empty bf16 tensor on a GPU")
-    K = w.shape[-1]
+    *lead, K = w.shape
     if group not in (32, 64, 128) or K % group:
         raise ValueError("group must be 32, 64 or 128 and divide the last dimension")
-    codes = torch.empty((*w.shape[:-1], K // 2), dtype=torch.uint8, device=w.device)
-    scales = torch.empty((*w.shape[:-1], K // group), dtype=torch.bfloat16, device=w.device)
-    zeros = torch.empty(scales.shape, dtype=torch.uint8, device=w.device) if zero_points else None
-    with _on_device(w.device):
-        st = moe_quantize_w4(w.data_ptr(), w.numel() // K, K, group, codes.data_ptr(), scales.data_ptr(), _ptr(zeros),
-                             torch.cuda.current_stream(w.device).cuda_stream)
-    if st != MOE_OK:
-        raise RuntimeError(moe_status_string(st))
+    dev = w.device
+    codes = torch.empty((*lead, K // 2), dtype=torch.uint8, device=dev)
+    scales = torch.empty((*lead, K // group), dtype=torch.bfloat16, device=dev)
+    zeros = torch.empty((*lead, K // group), dtype=torch.uint8, device=dev) if zero_points else None
+    _call(gpu, LIB.moe_quantize_w4, w.data_ptr(), w.numel() // K, K, group, codes.data_ptr(), scales.data_ptr(),
+          _ptr(zeros))
     return codes, scales, zeros
 
 
@@ -423,14 +453,12 @@ def dequantize_w4(codes, scales, zeros=None):
     import torch
     if codes.dim() < 1 or codes.numel() == 0:
         raise ValueError("dequantize_w4 takes non-empty codes")
-    group = _w4_group(codes, scales, zeros, codes.device)
-    K = 2 * codes.shape[-1]
-    out = torch.empty((*codes.shape[:-1], K), dtype=torch.bfloat16, device=codes.device)
-    with _on_device(codes.device):
-        st = moe_dequantize_w4(codes.data_ptr(), scales.data_ptr(), _ptr(zeros), out.numel() // K, K, group,
-                               out.data_ptr(), torch.cuda.current_stream(codes.device).cuda_stream)
-    if st != MOE_OK:
-        raise RuntimeError(moe_status_string(st))
+    gpu = _gpu_of(codes)
+    group = _w4_group(codes, scales, zeros, gpu)
+    *lead, half = codes.shape
+    out = torch.empty((*lead, 2 * half), dtype=torch.bfloat16, device=codes.device)
+    _call(gpu, LIB.moe_dequantize_w4, codes.data_ptr(), scales.data_ptr(), _ptr(zeros), codes.numel() // half, 2 * half,
+          group, out.data_ptr())
     return out
 
 
@@ -439,23 +467,21 @@ def linear_w4(x, codes, scales, zeros=None, bias=None):
     [N, K/group]) transposed, plus bias [N] bf16 or None: [M, N] bf16.  Made
     for a few rows (the codes are read once per 64)."""
     import torch
-    dev = x.device
-    if x.dtype != torch.bfloat16 or not x.is_cuda or not x.is_contiguous() or x.dim() != 2 or x.numel() == 0:
+    gpu = _gpu_of(x)
+    if gpu < 0 or not _on(x, gpu, torch.bfloat16) or x.dim() != 2 or x.numel() == 0:
         raise ValueError("linear_w4 takes a contiguous, non-empty bf16 [M, K] tensor on a GPU")
-    group = _w4_group(codes, scales, zeros, dev)
+    if codes.dim() != 2 or codes.numel() == 0:
+        raise ValueError("linear_w4 takes non-empty codes [N, K/2]")
+    group = _w4_group(codes, scales, zeros, gpu)
     M, K = x.shape
-    N = codes.shape[0]
-    if codes.dim() != 2 or 2 * codes.shape[1] != K or N < 1:
+    N, half = codes.shape
+    if 2 * half != K:
         raise ValueError("inconsistent shapes of x and the 4-bit weight")
-    if bias is not None and (bias.dtype != torch.bfloat16 or bias.shape != (N,) or bias.device != dev
-                             or not bias.is_contiguous()):
+    if bias is not None and (not _on(bias, gpu, torch.bfloat16) or bias.shape != (N,)):
         raise ValueError("bias must be a contiguous bf16 [N] on the same GPU")
-    y = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    with _on_device(dev):
-        st = moe_linear_w4(x.data_ptr(), M, codes.data_ptr(), scales.data_ptr(), _ptr(zeros), N, K, group, _ptr(bias),
-                           y.data_ptr(), torch.cuda.current_stream(dev).cuda_stream)
-    if st != MOE_OK:
-        raise RuntimeError(moe_status_string(st))
+    y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    _call(gpu, LIB.moe_linear_w4, x.data_ptr(), M, codes.data_ptr(), scales.data_ptr(), _ptr(zeros), N, K, group,
+          _ptr(bias), y.data_ptr())
     return y
 
 
@@ -466,35 +492,20 @@ def forward_decode_w4(x, W_g, W1, W1s, W1z, b1, W2, W2s, W2z, b2, k: int, n_shar
     both; x, W_g and the biases bf16.  ``workspace``: at least
     ``moe_workspace_bytes_decode_w4(T, d, h, E, k, n_shared)`` bytes, or None."""
     import torch
-    dev = x.device
-    for t in (x, W_g, b1, b2):
-        if t is not None and (t.dtype != torch.bfloat16 or not t.is_cuda or t.device != dev or not t.is_contiguous()):
-            raise ValueError("x, W_g, b1 and b2 of the 4-bit layer must be contiguous bf16 tensors on one GPU")
-    if activation not in ACTIVATIONS:
-        raise ValueError(f"activation must be one of {sorted(ACTIVATIONS)}")
-    group = _w4_group(W1, W1s, W1z, dev)
-    if _w4_group(W2, W2s, W2z, dev) != group:
+    if x.dtype is not torch.bfloat16:
+        raise ValueError("x, W_g and the biases of the 4-bit layer must be bf16")
+    gpu = _gpu_of(x)
+    group = _w4_group(W1, W1s, W1z, gpu)
+    if _w4_group(W2, W2s, W2z, gpu) != group:
         raise ValueError("W1 and W2 must have one group size")
     T, d = x.shape
     E, h, S = W_g.shape[0], W1.shape[1], n_shared
-    if W_g.shape != (E, d) or W1.shape != (E + S, h, d // 2) or W2.shape != (E + S, d, h // 2) or \
-            d % group or h % group or \
-            (b1 is not None and b1.shape != (E + S, h)) or (b2 is not None and b2.shape != (E + S, d)):
+    if W1.shape != (E + S, h, d // 2) or W2.shape != (E + S, d, h // 2) or d % group or h % group:
         raise ValueError("inconsistent shapes")
-    if b_g is not None and (b_g.dtype != torch.float32 or b_g.shape != (E,) or b_g.device != dev
-                            or not b_g.is_contiguous()):
-        raise ValueError("b_g must be a contiguous float32 [E] on the same GPU")
-    _check_b_sel(b_sel, E, dev)
-    nbytes = moe_workspace_bytes_decode_w4(T, d, h, E, k, S)
-    out, topk_idx, topk_w, workspace = _decode_outputs(x, k, nbytes, workspace)
-    launch = _decode_launch(x, h, MOE_BF16, b_g, b_sel, activation, workspace)
-    with _on_device(dev):
-        status = moe_forward_decode_w4(x.data_ptr(), W_g.data_ptr(), W1.data_ptr(), W1s.data_ptr(), _ptr(W1z),
-                                       _ptr(b1), W2.data_ptr(), W2s.data_ptr(), _ptr(W2z), _ptr(b2), group, E, k, S,
-                                       out.data_ptr(), topk_idx.data_ptr(), topk_w.data_ptr(), launch)
-    if status != MOE_OK:
-        raise RuntimeError(moe_status_string(status))
-    return DecodeOutput(out, topk_idx, topk_w)
+    return _decode(LIB.moe_forward_decode_w4, x, W_g,
+                   (W1.data_ptr(), W1s.data_ptr(), _ptr(W1z), _ptr(b1), W2.data_ptr(), W2s.data_ptr(), _ptr(W2z),
+                    _ptr(b2)), b1, W1, b2, k, S, b_g, b_sel, activation, 0, workspace,
+                   _decode_bytes_w4(T, d, h, E, k, S), (group,))
 
 
 __all__ = ["forward_decode", "forward_decode_w4", "DecodeOutput", "quantize_w4", "dequantize_w4", "linear_w4",

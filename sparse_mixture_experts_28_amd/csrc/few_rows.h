@@ -298,33 +298,40 @@ __device__ __forceinline__ void multiply_step(floatx4 (&acc)[NT][RT], const WBat
     for (int r = 0; r < RT; ++r) {
       u32x4 c = b.w[u][r];
       arrange_codes<F>(c);
+      floatx4 t[NT][kG];   // the groups' products are independent: all are under way before the first is used
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int g = 0; g < kG; ++g) t[j][g] = n136[j][g];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+          const bf16x8 cv = codes_to_bf16(c[g * kPer + i], base);
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            t[j][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[j][g * kPer + i]), cv, t[j][g], 0, 0, 0);
+        }
 #pragma unroll
       for (int g = 0; g < kG; ++g) {
         const int si = u * kG + g;
-        bf16x8 cv[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) cv[i] = codes_to_bf16(c[g * kPer + i], base);
         const uint32_t sw = si % 2 ? b.sc[r][si / 2] & 0xffff0000u : b.sc[r][si / 2] << 16;
         const float s = __uint_as_float(sw & live(g));
         float zf = 0.f;
         if constexpr (has_zeros(F))
           zf = static_cast<float>((b.zc[r][si / 4] >> (8 * (si % 4))) & 15u) * (1.f / 136.f) - 8.f / 136.f;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          floatx4 t = n136[j][g];
-#pragma unroll
-          for (int i = 0; i < kPer; ++i)
-            t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[j][g * kPer + i]), cv[i], t, 0, 0, 0);
+        for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            if constexpr (has_zeros(F)) t[i] = fmaf(zf, n136[j][g][i], t[i]);
-            acc[j][r][i] = fmaf(s, t[i], acc[j][r][i]);
+            if constexpr (has_zeros(F)) t[j][g][i] = fmaf(zf, n136[j][g][i], t[j][g][i]);
+            acc[j][r][i] = fmaf(s, t[j][g][i], acc[j][r][i]);
           }
-          // the sums stay here: moved behind the loop's branches, they would
-          // keep every group's products in registers until then
-          __asm__ volatile("" : "+v"(acc[j][r]));
-        }
       }
+      // the sums stay here: moved behind the loop's branches, they would keep
+      // every group's products in registers until then
+#pragma unroll
+      for (int j = 0; j < NT; ++j) __asm__ volatile("" : "+v"(acc[j][r]));
     }
   }
 }

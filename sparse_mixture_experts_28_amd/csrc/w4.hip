@@ -145,6 +145,132 @@ __global__ __launch_bounds__(NW * 64) void w4_linear_kernel(const uint16_t* x, W
   }
 }
 
+// The same for 17 to 64 rows: every step's activations are dense, so they come
+// straight from memory (L2) into operand registers, a tile of 16 rows at a time and
+// the next tile's ahead of the products; a step's codes are unpacked once for all
+// tiles.  A workgroup takes 16 RT columns and splits k over its waves: each
+// activation is read once per workgroup.
+template <Fmt F, int NT, int RT, int NW>
+__global__ __launch_bounds__(NW * 64) void w4_linear_rows_kernel(const uint16_t* x, WMat w, const uint16_t* bias,
+                                                                 uint16_t* y, int M) {
+  constexpr int U = group_shift(F) == 7 ? 2 : 1;   // steps of a batch of weights: whole words of scales
+  constexpr int kG = 128 >> group_shift(F), kPer = 4 / kG;
+  __shared__ float red[NW][RT * 256];
+  const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), q = lane >> 4;
+  const int n0 = blockIdx.x * 16 * RT, m0 = blockIdx.y * 64;
+  const int rows = min(M - m0, 16 * NT);
+  const uint32_t pitch = static_cast<uint32_t>(w.K) * 2u;
+  const __amdgpu_buffer_rsrc_t xr =
+      make_rsrc(x + static_cast<size_t>(m0) * w.K, static_cast<uint32_t>(rows) * pitch);
+  const uint32_t xq = static_cast<uint32_t>(quarter_k<F>(q)) * 2u;
+  uint32_t xo[NT];
+  floatx4 acc[NT][RT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int p = j * 16 + (lane & 15);
+    xo[j] = p < rows ? static_cast<uint32_t>(p) * pitch + xq : kOut;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[j][r] = floatx4{0.f, 0.f, 0.f, 0.f};
+  }
+  const int nst = (w.K + 127) / 128, nb = (nst + U - 1) / U;
+  const int s0 = wave * nb / NW * U, s1 = min(nst, (wave + 1) * nb / NW * U);
+  const int kend = min(w.K, s1 * 128);
+  const WRows wr = rows_of<F, RT>(w, 0, n0, lane);
+  auto load_x = [&](u32x4 (&v)[4], int s, int j) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int k0 = s * 128 + mfma_k<F>(i);
+      v[i] = load16(xr, k0 < kend ? xo[j] : kOut, static_cast<uint32_t>(k0) * 2u);
+    }
+  };
+  const uint32_t base = code_base();
+  const u32x4 neg = {0xc308c308u, 0xc308c308u, 0xc308c308u, 0xc308c308u};   // -136
+  WBatch<F, RT, U> b;
+  u32x4 xv[2][4];
+  if (s0 < s1) {
+    b.load(wr, s0, kend, q);
+    load_x(xv[0], s0, 0);
+  }
+  for (int sb = s0; sb < s1; sb += U) {
+    WBatch<F, RT, U> cur = b;
+    if (sb + U < s1) b.load(wr, sb + U, kend, q);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int s = sb + u;
+      bf16x8 cv[RT][4];
+      float sc[RT][kG], zf[RT][kG];
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        u32x4 c = cur.w[u][r];
+        arrange_codes<F>(c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) cv[r][i] = codes_to_bf16(c[i], base);
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+          const int si = u * kG + g;
+          const uint32_t sw = si % 2 ? cur.sc[r][si / 2] & 0xffff0000u : cur.sc[r][si / 2] << 16;
+          sc[r][g] = s * 128 + (g << group_shift(F)) < kend ? __uint_as_float(sw) : 0.f;
+          zf[r][g] = 0.f;
+          if constexpr (has_zeros(F))
+            zf[r][g] = static_cast<float>((cur.zc[r][si / 4] >> (8 * (si % 4))) & 15u) * (1.f / 136.f) - 8.f / 136.f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int at = (u * NT + j) & 1;
+        load_x(xv[at ^ 1], j + 1 < NT ? s : s + 1, j + 1 < NT ? j + 1 : 0);
+        u32x4 xt[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xt[i] = to_code_order(xv[at][i]);
+#pragma unroll
+        for (int g = 0; g < kG; ++g) {
+          floatx4 n136 = {0.f, 0.f, 0.f, 0.f}, t[RT];
+#pragma unroll
+          for (int i = 0; i < kPer; ++i)
+            n136 = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xt[g * kPer + i]),
+                                                           __builtin_bit_cast(bf16x8, neg), n136, 0, 0, 0);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) t[r] = n136;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i)
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+              t[r] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, xt[g * kPer + i]),
+                                                             cv[r][g * kPer + i], t[r], 0, 0, 0);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if constexpr (has_zeros(F)) t[r][i] = fmaf(zf[r][g], n136[i], t[r][i]);
+              acc[j][r][i] = fmaf(sc[r][g], t[r][i], acc[j][r][i]);
+            }
+            __asm__ volatile("" : "+v"(acc[j][r]));   // no product waits behind the loop's branch (few_rows.h)
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    if (j * 16 >= rows) break;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) *reinterpret_cast<floatx4*>(&red[wave][(r * 64 + lane) * 4]) = acc[j][r];
+    __syncthreads();
+    for (int i = threadIdx.x; i < RT * 256; i += NW * 64) {
+      const int n = (i >> 8) * 16 + (i & 15), pr = (i >> 4) & 15;
+      const int p = j * 16 + pr;
+      if (p < rows && n0 + n < w.N) {
+        float v = 0.f;
+#pragma unroll
+        for (int k = 0; k < NW; ++k) v += red[k][(i >> 8) * 256 + ((pr >> 2) * 16 + (i & 15)) * 4 + (pr & 3)];
+        if (bias != nullptr) v += bf16_to_f32(bias[n0 + n]);
+        y[static_cast<size_t>(m0 + p) * w.N + n0 + n] = f32_to_bf16(v);
+      }
+    }
+    __syncthreads();
+  }
+}
+
 #ifndef LRT
 #define LRT 1
 #endif
@@ -155,20 +281,25 @@ __global__ __launch_bounds__(NW * 64) void w4_linear_kernel(const uint16_t* x, W
 #define LNW 8
 #endif
 #ifndef LRT4
-#define LRT4 2
+#define LRT4 4
 #endif
-#ifndef LU4
-#define LU4 2
+#ifndef LNW4
+#define LNW4 8
 #endif
+template <Fmt F, int NT>
+void launch_rows(const uint16_t* x, int M, const WMat& w, const uint16_t* bias, uint16_t* y, hipStream_t st) {
+  const dim3 grid((w.N + 16 * LRT4 - 1) / (16 * LRT4), (M + 63) / 64);
+  w4_linear_rows_kernel<F, NT, LRT4, LNW4><<<grid, LNW4 * 64, 0, st>>>(x, w, bias, y, M);
+}
 template <Fmt F>
 hipError_t launch_linear(const uint16_t* x, int M, const WMat& w, const uint16_t* bias, uint16_t* y, hipStream_t st) {
   const unsigned gy = (M + 63) / 64;
   if (M <= 16)
     w4_linear_kernel<F, 1, LRT, LU, LNW, 4864>
         <<<dim3((w.N + 16 * LRT - 1) / (16 * LRT), gy), LNW * 64, 0, st>>>(x, w, bias, y, M);
-  else
-    w4_linear_kernel<F, 4, LRT4, LU4, 8, 17424>
-        <<<dim3((w.N + 16 * LRT4 - 1) / (16 * LRT4), gy), 512, 0, st>>>(x, w, bias, y, M);
+  else if (M <= 32) launch_rows<F, 2>(x, M, w, bias, y, st);
+  else if (M <= 48) launch_rows<F, 3>(x, M, w, bias, y, st);
+  else launch_rows<F, 4>(x, M, w, bias, y, st);
   return hipGetLastError();
 }
 
