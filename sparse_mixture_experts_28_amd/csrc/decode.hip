@@ -431,16 +431,25 @@ struct Tickets {
 #define A_U 4
 #endif
 #ifndef B_U
-#define B_U 4
+#define B_U 2
 #endif
 #ifndef M_U
 #define M_U 2
 #endif
 #ifndef MB_U
-#define MB_U 4
+#define MB_U 2
 #endif
 #ifndef B64NT
 #define B64NT 3
+#endif
+#ifndef AHM
+#define AHM 0
+#endif
+#ifndef AHW
+#define AHW 0
+#endif
+#ifndef AHB
+#define AHB 1
 #endif
 #ifndef WGS
 #define WGS 2
@@ -452,7 +461,8 @@ template <Fmt F, int TMAX> struct Shape {
   static constexpr bool kW = is_w4(F), kMany = TMAX > 16;
   static constexpr int kRT1 = kW && !kMany ? A_RT : 1;
   static constexpr int kRT2 = kRT1;
-  static constexpr int kU = kW ? (kMany ? M_U : A_U) : kMany ? MB_U : B_U;
+  static constexpr int kU1 = kW ? (kMany ? M_U : A_U) : 4;
+  static constexpr int kU2 = kW ? A_U : kMany ? MB_U : B_U;
   static constexpr int kNT1 = !kMany || kW ? 1 : 2;
   static constexpr int kNT2 = kW ? 1 : F == Fmt::kF32 ? kNT1 : TMAX == 1 ? 1 : TMAX == 16 ? 2 : B64NT;
   static constexpr int kRows1 = TMAX == 1 ? 1 : 16 * kNT1, kRows2 = TMAX == 1 ? (F == Fmt::kF32 ? 1 : 2) : 16 * kNT2;
@@ -460,6 +470,7 @@ template <Fmt F, int TMAX> struct Shape {
   static constexpr int kStep = kW ? 256 : 64;
   static constexpr int kStage = (TMAX == 1 ? (kW ? 2048 : 1024) : kRows * (kStep + 16)) + 32 + kStageZero;
   static constexpr int kWgs = WGS;
+  static constexpr bool kAhead2 = kW ? AHW : kMany ? AHM : AHB;
 };
 
 // a segment's products for one tile of tokens or for all NT (the others then
@@ -493,8 +504,8 @@ template <Fmt F, int TMAX>
 __global__ __launch_bounds__(kThreads, 4) void decode_phase1_kernel(DecodeArgs a) {
   using Sh = Shape<F, TMAX>;
   constexpr bool kBf = F != Fmt::kF32;
-  constexpr int NT = Sh::kNT1, RT = Sh::kRT1, U = Sh::kU, kN = 16 * RT;
-  using St = Stream<F, RT, U, true, Sh::kRows, Sh::kStage>;
+  constexpr int NT = Sh::kNT1, RT = Sh::kRT1, U = Sh::kU1, kN = 16 * RT;
+  using St = Stream<F, RT, U, false, true, Sh::kRows, Sh::kStage>;
   __shared__ Routing r;
   __shared__ float red[NT * RT * kWaves * 256];
   __shared__ __attribute__((aligned(16))) char stages[kWaves][Sh::kStage];
@@ -603,8 +614,8 @@ __global__ __launch_bounds__(kThreads, 4) void decode_phase2_kernel(DecodeArgs a
   using Sh = Shape<F, TMAX>;
   constexpr bool kBf = F != Fmt::kF32;
   constexpr int kTok = kBf ? 8 : 16;
-  constexpr int NT = Sh::kNT2, RT = Sh::kRT2, U = Sh::kU, kN = 16 * RT;
-  using St = Stream<F, RT, U, true, Sh::kRows, Sh::kStage>;
+  constexpr int NT = Sh::kNT2, RT = Sh::kRT2, U = Sh::kU2, kN = 16 * RT;
+  using St = Stream<F, RT, U, Sh::kAhead2, true, Sh::kRows, Sh::kStage>;
   __shared__ Routing r;
   __shared__ float tab[kWaves][TMAX * kN];
   __shared__ __attribute__((aligned(16))) char stages[kWaves][Sh::kStage];
@@ -772,9 +783,10 @@ int phase2_shape(int T, int* wgs) {
 
 // How a call's work is shared out; from the sizes alone, with the experts that
 // are taken when T tokens take k of E evenly.
-//   split    phase 2: shares of the sum per tile of output columns, one round of
-//            the grid or items of 1 MB, whichever makes more, of 32 KB at least
-//            and 64 at most
+//   split    phase 2: shares of the sum per tile of output columns: as many as fill
+//            one round of the grid, or of 1 MB where that makes three rounds and
+//            more (a second round that is mostly empty is the worst of both); of
+//            32 KB at least, 64 at most
 //   dynamic  2 MB or more to read per workgroup and phase
 DecodePlan decode_plan(int T, int d, int h, int E, int k, int S, int fmt) {
   int wgs = 0;
@@ -786,9 +798,9 @@ DecodePlan decode_plan(int T, int d, int h, int E, int k, int S, int fmt) {
   const int tiles = (d + 16 * rt - 1) / (16 * rt);
   const double tile_bytes = used * 16 * rt * h * elem;
   const int slots = 256 * wgs;
-  int sp = (slots + tiles - 1) / tiles;
+  int sp = tiles < slots ? slots / tiles : 1;
   const double by_size = tile_bytes / (1 << 20);
-  if (sp < by_size) sp = by_size < 64.0 ? static_cast<int>(by_size) : 64;
+  if (by_size >= 3.0 * sp) sp = by_size < 64.0 ? static_cast<int>(by_size) : 64;
   const double most = tile_bytes / 32768;
   if (sp > most) sp = most < 1.0 ? 1 : static_cast<int>(most);
   if (sp > 64) sp = 64;

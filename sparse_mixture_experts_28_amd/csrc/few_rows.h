@@ -349,10 +349,11 @@ __device__ __forceinline__ void multiply_step(floatx4 (&acc)[NT][RT], const WBat
 //
 // begin() issues the first loads, run() does the rest: called before the work
 // that ends the segment before (sums across waves, activation, stores), begin()
-// keeps the memory busy meanwhile.
+// keeps the memory busy meanwhile.  kAhead: run() loads a batch ahead of its
+// products too (registers for one more batch).
 constexpr int kStageZero = 16;
 
-template <Fmt F, int RT, int U, bool kOrdered, int SLOTS, int STAGE> struct Stream {
+template <Fmt F, int RT, int U, bool kAhead, bool kOrdered, int SLOTS, int STAGE> struct Stream {
   static constexpr int kStep = step_k(F) * act_bytes(F);     // activation bytes of a step and row
   static constexpr int kLoads = (STAGE - kStageZero + 1023) / 1024;
   static constexpr bool kDense = SLOTS * (U * kStep + 16) + kStageZero > STAGE;   // a chunk may be shorter than a batch
@@ -419,6 +420,11 @@ template <Fmt F, int RT, int U, bool kOrdered, int SLOTS, int STAGE> struct Stre
       store_x(stage, lane);
       int cb = s0;
       for (int s = s0;;) {
+        WBatch<F, RT, U> ready;
+        if constexpr (kAhead) {
+          ready = w;
+          if (s + U < s1) w.load(wr, s + U, kend, q);
+        }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
           if ((u == 0 || kDense) && s + u >= cb + steps && s + u < s1) {
@@ -435,13 +441,13 @@ template <Fmt F, int RT, int U, bool kOrdered, int SLOTS, int STAGE> struct Stre
               x[j][g] = *reinterpret_cast<const u32x4*>(s + u < s1 ? at : zero);
               if constexpr (is_w4(F) && !kOrdered) x[j][g] = to_code_order(x[j][g]);
             }
-          multiply_step<F, NT, RT, U>(acc, w, u, x, [&](int g) {
+          multiply_step<F, NT, RT, U>(acc, kAhead ? ready : w, u, x, [&](int g) {
             return (s + u) * step_k(F) + (g << group_shift(F)) < kend ? 0xffffffffu : 0u;
           });
         }
         s += U;
         if (s >= s1) break;
-        w.load(wr, s, kend, q);
+        if constexpr (!kAhead) w.load(wr, s, kend, q);
       }
     }
     // Wait states between the last products and whatever reads them, placed by

@@ -5,6 +5,9 @@
 //
 // q two to a byte along k (even k in the low nibble), s bf16, z uint8 or 8.
 #include "few_rows.h"
+#ifndef LAH
+#define LAH true
+#endif
 
 namespace moe {
 namespace {
@@ -108,7 +111,7 @@ __global__ __launch_bounds__(NW * 64) void w4_linear_kernel(const uint16_t* x, W
   const __amdgpu_buffer_rsrc_t xr =
       make_rsrc(x + static_cast<size_t>(m0) * w.K, static_cast<uint32_t>(rows) * pitch);
   char* mine = lds + wave * STAGE;
-  using St = Stream<F, RT, U, false, 16 * NT, STAGE>;
+  using St = Stream<F, RT, U, LAH, false, 16 * NT, STAGE>;
   St::clear(mine, lane);
   int rslot[NT];
   floatx4 acc[NT][RT];
