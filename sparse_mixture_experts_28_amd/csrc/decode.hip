@@ -424,54 +424,34 @@ struct Tickets {
   }
 };
 
-#ifndef A_RT
-#define A_RT 1
-#endif
-#ifndef A_U
-#define A_U 4
-#endif
-#ifndef B_U
-#define B_U 2
-#endif
-#ifndef M_U
-#define M_U 2
-#endif
-#ifndef MB_U
-#define MB_U 2
-#endif
-#ifndef B64NT
-#define B64NT 3
-#endif
-#ifndef AHM
-#define AHM 0
-#endif
-#ifndef AHW
-#define AHW 0
-#endif
-#ifndef AHB
-#define AHB 1
-#endif
-#ifndef WGS
-#define WGS 2
-#endif
-// Shapes of the phase kernels by format and token class: row tiles of a wave,
-// steps loaded together, tiles of tokens at once (an expert with more makes
-// several jobs), bytes of a wave's activation region, workgroups per CU.
+// Shapes of the phase kernels by format and token class (1, up to 16 and up to 64
+// tokens): steps loaded together, tiles of tokens at once (an expert with more
+// makes several jobs), waves that split k in phase 1 (the others take rows of their
+// own), bytes of a wave's activation region.  Two workgroups of eight waves per CU
+// (128 registers a wave, LDS for two).  Measured, phase 1 + phase 2 in us:
+//   steps    bf16, one token of the Mixtral shape: 2 + 2 steps 47 + 45, 4 + 4 43 +
+//            46, 4 + 2 a batch ahead 43 + 44, 8 + 8 44 + 50; 4-bit: 2 + 2 steps 22 +
+//            21, 4 + 4 21 + 20
+//   waves    4-bit, 64 tokens of the DeepSeek shape (57 KB of codes to a job and
+//            16 rows): 8 on k 597, 4 536, 2 with four steps 502, 1 579; bf16 lose
+//            by fewer (32 tokens: 8 743, 4 796)
+//   tiles    16 rows of weights to a wave; 32 lose everywhere (registers, and
+//            fewer loads on their way at the end)
+//   WGs      three per CU: 43 + 44 becomes 49 + 53 (one token, Mixtral shape)
 template <Fmt F, int TMAX> struct Shape {
   static constexpr bool kW = is_w4(F), kMany = TMAX > 16;
-  static constexpr int kRT1 = kW && !kMany ? A_RT : 1;
-  static constexpr int kRT2 = kRT1;
-  static constexpr int kU1 = kW ? (kMany ? M_U : A_U) : 4;
-  static constexpr int kU2 = kW ? A_U : kMany ? MB_U : B_U;
+  static constexpr int kRT1 = 1, kRT2 = 1;
+  static constexpr int kU1 = 4, kU2 = kW ? 4 : 2;
+  static constexpr bool kAhead2 = !kW && !kMany;
+  static constexpr int kSplit1 = kW && kMany ? 2 : 8;
   static constexpr int kNT1 = !kMany || kW ? 1 : 2;
-  static constexpr int kNT2 = kW ? 1 : F == Fmt::kF32 ? kNT1 : TMAX == 1 ? 1 : TMAX == 16 ? 2 : B64NT;
+  static constexpr int kNT2 = kW ? 1 : F == Fmt::kF32 ? kNT1 : TMAX == 1 ? 1 : TMAX == 16 ? 2 : 3;
   static constexpr int kRows1 = TMAX == 1 ? 1 : 16 * kNT1, kRows2 = TMAX == 1 ? (F == Fmt::kF32 ? 1 : 2) : 16 * kNT2;
   static constexpr int kRows = kRows1 > kRows2 ? kRows1 : kRows2;   // most rows staged
   static constexpr int kStep = kW ? 256 : 64;
   static constexpr int kStage = (TMAX == 1 ? (kW ? 2048 : 1024) : kRows * (kStep + 16)) + 32 + kStageZero;
-  static constexpr int kWgs = WGS;
-  static constexpr bool kAhead2 = kW ? AHW : kMany ? AHM : AHB;
 };
+constexpr int kWgs = 2;
 
 // a segment's products for one tile of tokens or for all NT (the others then
 // hold rows whose sums nobody reads)
@@ -496,15 +476,16 @@ __device__ __forceinline__ void run_tiles(St& st, floatx4 (&acc)[NT][RT], __amdg
 }
 
 // ------------------------------------------------------------------ phase 1 --
-// One item: a job and 16 RT hidden units.  The job's tokens are the activation
-// rows, NT tiles of 16; the waves split k and add their sums in LDS in wave
-// order.  The next item's first loads are issued before this one's sums, biases,
+// One item: a job and hidden units, 16 RT for each group of KS waves.  The job's
+// tokens are the activation rows, NT tiles of 16; a group's waves split k and add
+// their sums in LDS in wave order.  The next item's first loads are issued before this one's sums, biases,
 // activations and stores.
 template <Fmt F, int TMAX>
 __global__ __launch_bounds__(kThreads, 4) void decode_phase1_kernel(DecodeArgs a) {
   using Sh = Shape<F, TMAX>;
   constexpr bool kBf = F != Fmt::kF32;
-  constexpr int NT = Sh::kNT1, RT = Sh::kRT1, U = Sh::kU1, kN = 16 * RT;
+  constexpr int NT = Sh::kNT1, RT = Sh::kRT1, U = Sh::kU1, KS = Sh::kSplit1;
+  constexpr int kN = 16 * RT * (kWaves / KS);
   using St = Stream<F, RT, U, false, true, Sh::kRows, Sh::kStage>;
   __shared__ Routing r;
   __shared__ float red[NT * RT * kWaves * 256];
@@ -519,7 +500,7 @@ __global__ __launch_bounds__(kThreads, 4) void decode_phase1_kernel(DecodeArgs a
   const int ntile = (a.h + kN - 1) / kN;
   const int items = uniform(r.n) * ntile;
   const int nst = (a.d + step_k(F) - 1) / step_k(F), nb = (nst + U - 1) / U;
-  const int s0 = wave * nb / kWaves * U, s1 = min(nst, (wave + 1) * nb / kWaves * U);
+  const int ks = wave % KS, s0 = ks * nb / KS * U, s1 = min(nst, (ks + 1) * nb / KS * U);
   const uint32_t pitch = static_cast<uint32_t>(a.d) * act_bytes(F);
   const __amdgpu_buffer_rsrc_t xr = make_rsrc(is_w4(F) ? a.xord : a.x, static_cast<uint32_t>(a.T) * pitch);
   Tickets tk{a.counters, next, a.dynamic != 0, 0, 0};
@@ -532,7 +513,8 @@ __global__ __launch_bounds__(kThreads, 4) void decode_phase1_kernel(DecodeArgs a
     n0 = (item - job * ntile) * kN;
     o = uniform(r.off[job]);
     rows = uniform(r.off[job + 1]) - o;
-    st.begin(rows_of<F, RT>(a.W1, e, n0, lane), xr, soff, rows, s0, s1, a.d, lane);
+    const int nw = n0 + wave / KS * 16 * RT;   // the wave's own rows; none past the last
+    st.begin(rows_of<F, RT>(a.W1, e, min(nw, a.h), lane), xr, soff, rows, s0, nw < a.h ? s1 : s0, a.d, lane);
   };
   int item = blockIdx.x;
   if (item < items) begin(item);
@@ -556,15 +538,16 @@ __global__ __launch_bounds__(kThreads, 4) void decode_phase1_kernel(DecodeArgs a
     const int ce = e, cn0 = n0, co = o, crows = rows;
     item = tk.take();
     if (item < items) begin(item);
-    for (int i = threadIdx.x; i < tl * RT * 256; i += kThreads) {
-      // result (row p of the job's tokens, hidden unit n): lane (n, p / 4 % 4), register p % 4
-      const int jr = i >> 8, n = cn0 + (jr % RT) * 16 + (i & 15), pr = (i >> 4) & 15;
-      const int p = jr / RT * 16 + pr;
+    for (int i = threadIdx.x; i < tl * 16 * kN; i += kThreads) {
+      // result (row p of the job's tokens, hidden unit n): row tile rt of the waves
+      // wg KS .., lane (n, p / 4 % 4), register p % 4
+      const int rt16 = i >> 8, j = rt16 / (kN / 16), wr = rt16 % (kN / 16), wg = wr / RT, rt = wr % RT;
+      const int n = cn0 + wr * 16 + (i & 15), pr = (i >> 4) & 15, p = j * 16 + pr;
       if (p >= crows || n >= a.h) continue;
-      const float* sum = red + (jr * kWaves * 64 + (pr >> 2) * 16 + (i & 15)) * 4 + (pr & 3);
+      const float* sum = red + (((j * RT + rt) * kWaves + wg * KS) * 64 + (pr >> 2) * 16 + (i & 15)) * 4 + (pr & 3);
       float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) v += sum[w * 256];
+      for (int w = 0; w < KS; ++w) v += sum[w * 256];
       if (a.b1 != nullptr) v += load1<kBf>(a.b1, static_cast<size_t>(ce) * a.h + n);
       v = a.act == MOE_ACT_SILU ? v / (1.f + expf(-v)) : 0.5f * v * (1.f + erff(v * 0.70710678118654752440f));
       const int t = r.row[co + p] & 255, slot = r.row[co + p] >> 8;
@@ -747,7 +730,7 @@ __global__ __launch_bounds__(kThreads, 4) void decode_phase2_kernel(DecodeArgs a
 // F: the format without zero points, Z: with them (the same where there are none)
 template <Fmt F, Fmt Z, int TMAX>
 hipError_t launch_phases(const DecodeArgs& a, hipStream_t st) {
-  const int grid = device_cu_count() * Shape<F, TMAX>::kWgs;
+  const int grid = device_cu_count() * kWgs;
   if (a.T > kWaves) decode_select_kernel<<<a.T, 64, 0, st>>>(a);
   if (a.W1.z != nullptr) decode_phase1_kernel<Z, TMAX><<<grid, kThreads, 0, st>>>(a);
   else decode_phase1_kernel<F, TMAX><<<grid, kThreads, 0, st>>>(a);
@@ -773,12 +756,6 @@ void launch_logits(const DecodeArgs& a, hipStream_t st) {
   else decode_logits_kernel<BF16, 16><<<dim3(a.E, (a.T + 15) / 16), threads, 0, st>>>(a);
 }
 
-template <Fmt F>
-int phase2_shape(int T, int* wgs) {
-  *wgs = T == 1 ? Shape<F, 1>::kWgs : T <= 16 ? Shape<F, 16>::kWgs : Shape<F, kMaxT>::kWgs;
-  return T == 1 ? Shape<F, 1>::kRT2 : T <= 16 ? Shape<F, 16>::kRT2 : Shape<F, kMaxT>::kRT2;
-}
-
 }  // namespace
 
 // How a call's work is shared out; from the sizes alone, with the experts that
@@ -789,15 +766,11 @@ int phase2_shape(int T, int* wgs) {
 //            32 KB at least, 64 at most
 //   dynamic  2 MB or more to read per workgroup and phase
 DecodePlan decode_plan(int T, int d, int h, int E, int k, int S, int fmt) {
-  int wgs = 0;
-  const int rt = fmt == kDecodeF32 ? phase2_shape<Fmt::kF32>(T, &wgs)
-                                   : fmt == kDecodeBf16 ? phase2_shape<Fmt::kBf16>(T, &wgs)
-                                                        : phase2_shape<Fmt::kW4g128>(T, &wgs);
   const double used = E * (1.0 - std::pow(1.0 - static_cast<double>(k) / E, T)) + S;
   const double elem = fmt == kDecodeF32 ? 4.0 : fmt == kDecodeBf16 ? 2.0 : 0.5;
-  const int tiles = (d + 16 * rt - 1) / (16 * rt);
-  const double tile_bytes = used * 16 * rt * h * elem;
-  const int slots = 256 * wgs;
+  const int tiles = (d + 15) / 16;
+  const double tile_bytes = used * 16 * h * elem;
+  const int slots = 256 * kWgs;
   int sp = tiles < slots ? slots / tiles : 1;
   const double by_size = tile_bytes / (1 << 20);
   if (by_size >= 3.0 * sp) sp = by_size < 64.0 ? static_cast<int>(by_size) : 64;
