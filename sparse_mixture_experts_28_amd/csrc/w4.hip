@@ -5,70 +5,109 @@
 //
 // q two to a byte along k (even k in the low nibble), s bf16, z uint8 or 8.
 #include "few_rows.h"
-#ifndef LAH
-#define LAH true
-#endif
 
 namespace moe {
 namespace {
 
 // ---------------------------------------------------------------- quantize --
 // A lane takes 8 consecutive elements, a group is group / 8 neighbouring lanes.
-// Quotients of bf16 numbers never fall within float32 rounding of a tie without
-// being one (both significands have 8 bits), so float32 division decides every
-// code as exact arithmetic does.
-__device__ __forceinline__ float group_max(float v, int lanes) {
-  for (int o = lanes >> 1; o >= 1; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+// Magnitudes are compared as integers (the same order, and an infinity or NaN
+// comes out on top).  Maxima over 4, 8 or 16 lanes by row moves: lane ^ 1, lane ^
+// 2, then the mirrors, which after the first two pair the same partial results as
+// lane ^ 4 and lane ^ 8.
+template <int CTRL>
+__device__ __forceinline__ int dpp_max(int v) {
+  return max(v, __builtin_amdgcn_mov_dpp(v, CTRL, 0xF, 0xF, false));
+}
+template <int LANES>
+__device__ __forceinline__ int group_max(int v) {
+  v = dpp_max<0xB1>(v);
+  v = dpp_max<0x4E>(v);
+  if constexpr (LANES >= 8) v = dpp_max<0x141>(v);
+  if constexpr (LANES >= 16) v = dpp_max<0x140>(v);
   return v;
 }
 
-template <bool ZERO>
-__global__ __launch_bounds__(256) void w4_quantize_kernel(const uint16_t* src, long long n8, int gshift,
-                                                          uint32_t* codes, uint16_t* scales, uint8_t* zeros) {
-  const int lanes = 1 << (gshift - 3);
-  const long long stride = static_cast<long long>(gridDim.x) * blockDim.x;
-  // n8 is a multiple of the lanes of a group, so a group is in or out as a whole
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < n8; i += stride) {
-    const u32x4 raw = reinterpret_cast<const u32x4*>(src)[i];
-    float v[8];
+// round(v / s) for a bf16 s > 0 and a bf16 v of at most a few times s, ties to
+// even, as exact arithmetic rounds it.  s = m 2^e with m in [1/2, 1), r ~ 1 / m:
+// the corrected quotient is within a few units in its last place, and exact where
+// the quotient is a float32 number; two 8-bit significands have no quotient within
+// 2^-9 of a tie k + 1/2 that is not the tie.  (The division of the library takes
+// three times the instructions.)
+__device__ __forceinline__ float round_quotient(float v, float m, float r, int e) {
+  const float n = ldexpf(v, -e);
+  float q = n * r;
+  q = fmaf(fmaf(-q, m, n), r, q);
+  return rintf(q);
+}
+
+template <int GSHIFT, bool ZERO>
+__device__ __forceinline__ void quantize8(u32x4 raw, long long i, uint32_t* codes, uint16_t* scales, uint8_t* zeros) {
+  constexpr int kLanes = 1 << (GSHIFT - 3);
+  constexpr int kInf = 0x7f800000;
+  int v[8];   // the elements' float32 bits
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      v[2 * m] = __uint_as_float(raw[m] << 16);
-      v[2 * m + 1] = __uint_as_float(raw[m] & 0xffff0000u);
-    }
-    float hi = 0.f, lo = 0.f, bad = 0.f;   // lo: the largest -v
+  for (int m = 0; m < 4; ++m) {
+    v[2 * m] = static_cast<int>(raw[m] << 16);
+    v[2 * m + 1] = static_cast<int>(raw[m] & 0xffff0000u);
+  }
+  int hi = 0, lo = 0;   // the largest v and the largest -v, at least 0; symmetric: hi of both
 #pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      bad = fabsf(v[m]) < INFINITY ? bad : 1.f;
-      hi = fmaxf(hi, v[m]);
-      lo = fmaxf(lo, -v[m]);
-    }
-    hi = group_max(hi, lanes);
-    lo = group_max(lo, lanes);
-    bad = group_max(bad, lanes);
-    uint16_t sb;
-    float z = 8.f;
+  for (int m = 0; m < 8; ++m) {
     if constexpr (ZERO) {
-      sb = f32_to_bf16(static_cast<float>((static_cast<double>(hi) + static_cast<double>(lo)) / 15.0));
+      hi = max(hi, v[m]);
+      lo = max(lo, v[m] ^ static_cast<int>(0x80000000u));
     } else {
-      sb = f32_to_bf16(fmaxf(hi, lo) / 7.f);
+      hi = max(hi, v[m] & 0x7fffffff);
     }
-    if (bad != 0.f) sb = 0x7fc0;   // a group with an infinity or NaN has no scale
-    const float s = bf16_to_f32(sb);
-    const bool fine = s > 0.f;      // false: all zero (or too small for a scale), or NaN
-    if constexpr (ZERO) z = fine ? fminf(rintf(lo / s), 15.f) : 0.f;
-    uint32_t c = 0;
+  }
+  hi = group_max<kLanes>(hi);
+  if constexpr (ZERO) lo = group_max<kLanes>(lo);
+  uint16_t sb;
+  if constexpr (ZERO) {
+    // the quotient by 15 in float64, corrected as above
+    const double d = static_cast<double>(__int_as_float(hi)) + static_cast<double>(__int_as_float(lo));
+    double q = d * (1.0 / 15.0);
+    q = fma(fma(-q, 15.0, d), 1.0 / 15.0, q);
+    sb = f32_to_bf16(static_cast<float>(q));
+  } else {
+    sb = f32_to_bf16(__int_as_float(hi) / 7.f);
+  }
+  if (hi >= kInf || lo >= kInf) sb = 0x7fc0;   // a group with an infinity or NaN has no scale
+  const float s = bf16_to_f32(sb);
+  const bool fine = s > 0.f;      // false: all zero (or too small for a scale), or NaN
+  int e;
+  const float m2 = frexpf(fine ? s : 1.f, &e);
+  const float r = __builtin_amdgcn_rcpf(m2);
+  float z = 8.f;
+  if constexpr (ZERO) z = fine ? fminf(round_quotient(__int_as_float(lo), m2, r, e), 15.f) : 0.f;
+  uint32_t c = 0;
 #pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      const float q = fine ? fminf(fmaxf(rintf(v[m] / s) + z, 0.f), 15.f) : z;
-      c |= static_cast<uint32_t>(q) << (4 * m);
-    }
-    codes[i] = c;
-    if ((threadIdx.x & (lanes - 1)) == 0) {
-      const long long g = i >> (gshift - 3);
-      scales[g] = sb;
-      if constexpr (ZERO) zeros[g] = static_cast<uint8_t>(z);
-    }
+  for (int m = 0; m < 8; ++m) {
+    const float q = fminf(fmaxf(round_quotient(__int_as_float(v[m]), m2, r, e) + z, 0.f), 15.f);
+    c |= static_cast<uint32_t>(fine ? q : z) << (4 * m);
+  }
+  codes[i] = c;
+  if ((threadIdx.x & (kLanes - 1)) == 0) {
+    const long long g = i >> (GSHIFT - 3);
+    scales[g] = sb;
+    if constexpr (ZERO) zeros[g] = static_cast<uint8_t>(z);
+  }
+}
+
+// Two runs of 8 elements a thread, both loaded first.  n8 is a multiple of the
+// lanes of a group, so a group is in or out as a whole.
+template <int GSHIFT, bool ZERO>
+__global__ __launch_bounds__(256) void w4_quantize_kernel(const uint16_t* src, long long n8, uint32_t* codes,
+                                                          uint16_t* scales, uint8_t* zeros) {
+  const long long stride = static_cast<long long>(gridDim.x) * 512;
+  for (long long i = static_cast<long long>(blockIdx.x) * 512 + threadIdx.x; i < n8; i += stride) {
+    const u32x4 a = reinterpret_cast<const u32x4*>(src)[i];
+    const bool two = i + 256 < n8;
+    u32x4 b = {0u, 0u, 0u, 0u};
+    if (two) b = reinterpret_cast<const u32x4*>(src)[i + 256];
+    quantize8<GSHIFT, ZERO>(a, i, codes, scales, zeros);
+    if (two) quantize8<GSHIFT, ZERO>(b, i + 256, codes, scales, zeros);
   }
 }
 
@@ -95,64 +134,53 @@ __global__ __launch_bounds__(256) void w4_dequantize_kernel(const uint32_t* code
 }
 
 // ------------------------------------------------------------------ Linear --
-// y[m, n] = sum_k x[m, k] w[n, k] + b[n].  One workgroup per 16 columns and 64
-// rows; its waves split k and add their sums in LDS in wave order.
-template <Fmt F, int NT, int RT, int U, int NW, int STAGE>
+// y[m, n] = sum_k x[m, k] w[n, k] + b[n] for up to 16 rows.  One workgroup per 16
+// columns; its waves split k and add their sums in LDS in wave order.
+template <Fmt F, int U, int NW, int STAGE>
 __global__ __launch_bounds__(NW * 64) void w4_linear_kernel(const uint16_t* x, WMat w, const uint16_t* bias,
                                                             uint16_t* y, int M) {
   // the waves' activation regions, then their sums
-  constexpr int kSums = NT * RT * NW * 1024;
-  __shared__ __attribute__((aligned(16))) char lds[NW * STAGE > kSums ? NW * STAGE : kSums];
+  static_assert(STAGE >= 1024, "a wave's sums fit its region");
+  __shared__ __attribute__((aligned(16))) char lds[NW * STAGE];
   float* red = reinterpret_cast<float*>(lds);
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-  const int n0 = blockIdx.x * 16 * RT, m0 = blockIdx.y * 64;
-  const int rows = min(M - m0, 64);
+  const int n0 = blockIdx.x * 16;
   const uint32_t pitch = static_cast<uint32_t>(w.K) * 2u;
-  const __amdgpu_buffer_rsrc_t xr =
-      make_rsrc(x + static_cast<size_t>(m0) * w.K, static_cast<uint32_t>(rows) * pitch);
+  const __amdgpu_buffer_rsrc_t xr = make_rsrc(x, static_cast<uint32_t>(M) * pitch);
   char* mine = lds + wave * STAGE;
-  using St = Stream<F, RT, U, LAH, false, 16 * NT, STAGE>;
+  using St = Stream<F, 1, U, true, false, 16, STAGE>;
   St::clear(mine, lane);
-  int rslot[NT];
-  floatx4 acc[NT][RT];
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    rslot[j] = min(j * 16 + (lane & 15), rows - 1);
-#pragma unroll
-    for (int r = 0; r < RT; ++r) acc[j][r] = floatx4{0.f, 0.f, 0.f, 0.f};
-  }
-  const int tl = (rows + 15) / 16;
   const int nst = (w.K + 127) / 128, nb = (nst + U - 1) / U;
   const int s0 = wave * nb / NW * U, s1 = min(nst, (wave + 1) * nb / NW * U);
   auto soff = [&](int slot) { return static_cast<uint32_t>(slot) * pitch; };
   St st;
-  st.begin(rows_of<F, RT>(w, 0, n0, lane), xr, soff, rows, s0, s1, w.K, lane);
+  st.begin(rows_of<F, 1>(w, 0, n0, lane), xr, soff, M, s0, s1, w.K, lane);
+  floatx4 acc[1][1] = {{floatx4{0.f, 0.f, 0.f, 0.f}}};
+  const int rslot[1] = {min(lane & 15, M - 1)};
   st.run(acc, xr, soff, rslot, mine, lane);
   __syncthreads();
-#pragma unroll
-  for (int j = 0; j < NT; ++j)
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-      *reinterpret_cast<floatx4*>(red + (((j * RT + r) * NW + wave) * 64 + lane) * 4) = acc[j][r];
+  *reinterpret_cast<floatx4*>(red + (wave * 64 + lane) * 4) = acc[0][0];
   __syncthreads();
-  for (int i = threadIdx.x; i < tl * RT * 256; i += NW * 64) {
-    const int jr = i >> 8, n = (jr % RT) * 16 + (i & 15), pr = (i >> 4) & 15;
-    const int p = jr / RT * 16 + pr;
-    if (p >= rows || n0 + n >= w.N) continue;
-    const float* s = red + (jr * NW * 64 + (pr >> 2) * 16 + (i & 15)) * 4 + (pr & 3);
+  // result (row p, column n): lane (n, p / 4), register p % 4
+  const int n = threadIdx.x & 15, p = threadIdx.x >> 4;
+  if (p < M && p < 16 && n0 + n < w.N) {
+    const float* s = red + ((p >> 2) * 16 + n) * 4 + (p & 3);
     float v = 0.f;
 #pragma unroll
     for (int q = 0; q < NW; ++q) v += s[q * 256];
     if (bias != nullptr) v += bf16_to_f32(bias[n0 + n]);
-    y[static_cast<size_t>(m0 + p) * w.N + n0 + n] = f32_to_bf16(v);
+    y[static_cast<size_t>(p) * w.N + n0 + n] = f32_to_bf16(v);
   }
 }
 
 // The same for 17 to 64 rows: every step's activations are dense, so they come
 // straight from memory (L2) into operand registers, a tile of 16 rows at a time and
 // the next tile's ahead of the products; a step's codes are unpacked once for all
-// tiles.  A workgroup takes 16 RT columns and splits k over its waves: each
-// activation is read once per workgroup.
+// tiles.  A workgroup takes 16 RT columns of up to 64 rows and splits k over its
+// waves: each activation is read once per workgroup.  37 rows, 14335 columns, K =
+// 4096, groups of 32 with zero points: 28 us with RT = 4, 32 with 2, 56 with 1; the
+// activations staged in LDS as for fewer rows 47 to 74.  Bound by the vector
+// operations on the group sums (half of its time) and their waits.
 template <Fmt F, int NT, int RT, int NW>
 __global__ __launch_bounds__(NW * 64) void w4_linear_rows_kernel(const uint16_t* x, WMat w, const uint16_t* bias,
                                                                  uint16_t* y, int M) {
@@ -274,32 +302,15 @@ __global__ __launch_bounds__(NW * 64) void w4_linear_rows_kernel(const uint16_t*
   }
 }
 
-#ifndef LRT
-#define LRT 1
-#endif
-#ifndef LU
-#define LU 4
-#endif
-#ifndef LNW
-#define LNW 8
-#endif
-#ifndef LRT4
-#define LRT4 4
-#endif
-#ifndef LNW4
-#define LNW4 8
-#endif
 template <Fmt F, int NT>
 void launch_rows(const uint16_t* x, int M, const WMat& w, const uint16_t* bias, uint16_t* y, hipStream_t st) {
-  const dim3 grid((w.N + 16 * LRT4 - 1) / (16 * LRT4), (M + 63) / 64);
-  w4_linear_rows_kernel<F, NT, LRT4, LNW4><<<grid, LNW4 * 64, 0, st>>>(x, w, bias, y, M);
+  const dim3 grid((w.N + 63) / 64, (M + 63) / 64);
+  w4_linear_rows_kernel<F, NT, 4, 8><<<grid, 512, 0, st>>>(x, w, bias, y, M);
 }
 template <Fmt F>
 hipError_t launch_linear(const uint16_t* x, int M, const WMat& w, const uint16_t* bias, uint16_t* y, hipStream_t st) {
-  const unsigned gy = (M + 63) / 64;
   if (M <= 16)
-    w4_linear_kernel<F, 1, LRT, LU, LNW, 4864>
-        <<<dim3((w.N + 16 * LRT - 1) / (16 * LRT), gy), LNW * 64, 0, st>>>(x, w, bias, y, M);
+    w4_linear_kernel<F, 4, 8, 4864><<<dim3((w.N + 15) / 16), 512, 0, st>>>(x, w, bias, y, M);
   else if (M <= 32) launch_rows<F, 2>(x, M, w, bias, y, st);
   else if (M <= 48) launch_rows<F, 3>(x, M, w, bias, y, st);
   else launch_rows<F, 4>(x, M, w, bias, y, st);
@@ -316,8 +327,14 @@ int grid_of(long long n8) {
 hipError_t launch_w4_quantize(const uint16_t* src, long long n, int gshift, uint8_t* codes, uint16_t* scales,
                               uint8_t* zeros, hipStream_t st) {
   uint32_t* c = reinterpret_cast<uint32_t*>(codes);
-  if (zeros != nullptr) w4_quantize_kernel<true><<<grid_of(n / 8), 256, 0, st>>>(src, n / 8, gshift, c, scales, zeros);
-  else w4_quantize_kernel<false><<<grid_of(n / 8), 256, 0, st>>>(src, n / 8, gshift, c, scales, zeros);
+  const long long n8 = n / 8;
+  const int grid = grid_of((n8 + 1) / 2);
+  if (gshift == 5 && zeros) w4_quantize_kernel<5, true><<<grid, 256, 0, st>>>(src, n8, c, scales, zeros);
+  else if (gshift == 5) w4_quantize_kernel<5, false><<<grid, 256, 0, st>>>(src, n8, c, scales, zeros);
+  else if (gshift == 6 && zeros) w4_quantize_kernel<6, true><<<grid, 256, 0, st>>>(src, n8, c, scales, zeros);
+  else if (gshift == 6) w4_quantize_kernel<6, false><<<grid, 256, 0, st>>>(src, n8, c, scales, zeros);
+  else if (zeros) w4_quantize_kernel<7, true><<<grid, 256, 0, st>>>(src, n8, c, scales, zeros);
+  else w4_quantize_kernel<7, false><<<grid, 256, 0, st>>>(src, n8, c, scales, zeros);
   return hipGetLastError();
 }
 
