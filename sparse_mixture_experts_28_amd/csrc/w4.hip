@@ -248,7 +248,7 @@ __global__ __launch_bounds__(NW * 64) void w4_linear_rows_kernel(const uint16_t*
       }
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const int at = (u * NT + j) & 1;
+        const int at = j & 1;
         load_x(xv[at ^ 1], j + 1 < NT ? s : s + 1, j + 1 < NT ? j + 1 : 0);
         u32x4 xt[4];
 #pragma unroll
@@ -278,6 +278,10 @@ __global__ __launch_bounds__(NW * 64) void w4_linear_rows_kernel(const uint16_t*
             __asm__ volatile("" : "+v"(acc[j][r]));   // no product waits behind the loop's branch (few_rows.h)
           }
         }
+      }
+      if constexpr (NT % 2 != 0) {   // the next step starts at xv[0] again
+#pragma unroll
+        for (int i = 0; i < 4; ++i) xv[0][i] = xv[1][i];
       }
     }
   }

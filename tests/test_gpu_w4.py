@@ -74,7 +74,9 @@ def test_quantize_and_read_back(shape, group, zero_points):
 @pytest.mark.parametrize("zeros", [False, True])
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("M,N,kg", [(1, 1, 1), (1, 4096, 4), (2, 17, 3), (5, 333, 9), (16, 64, 33), (17, 100, 5),
-                                    (37, 515, 8), (64, 31, 12), (65, 48, 2), (130, 20, 7)])
+                                    (37, 515, 8), (64, 31, 12), (65, 48, 2), (130, 20, 7),
+                                    (20, 90, 101), (37, 100, 100), (48, 65, 130), (64, 70, 67), (100, 33, 99), (40, 4130, 66),
+                                    (33, 8200, 34), (65, 8191, 9)])
 def test_linear(M, N, kg, group, zeros):
     import sparse_mixture_experts_28_amd as moe
     K = kg * group
