@@ -178,9 +178,9 @@ __global__ __launch_bounds__(NW * 64) void w4_linear_kernel(const uint16_t* x, W
 // the next tile's ahead of the products; a step's codes are unpacked once for all
 // tiles.  A workgroup takes 16 RT columns of up to 64 rows and splits k over its
 // waves: each activation is read once per workgroup.  37 rows, 14335 columns, K =
-// 4096, groups of 32 with zero points: 28 us with RT = 4, 32 with 2, 56 with 1; the
-// activations staged in LDS as for fewer rows 47 to 74.  Bound by the vector
-// operations on the group sums (half of its time) and their waits.
+// 4096, groups of 32 with zero points: 27 us; the activations staged in LDS as for
+// fewer rows 47 to 74.  Bound by the vector operations on the group sums (half of
+// its time) and their waits.
 template <Fmt F, int NT, int RT, int NW>
 __global__ __launch_bounds__(NW * 64) void w4_linear_rows_kernel(const uint16_t* x, WMat w, const uint16_t* bias,
                                                                  uint16_t* y, int M) {
@@ -306,10 +306,16 @@ __global__ __launch_bounds__(NW * 64) void w4_linear_rows_kernel(const uint16_t*
   }
 }
 
+// As few columns to a workgroup as still fit one round of 256 CUs.  Microseconds
+// with RT = 1, 2, 4 (37 rows, groups of 128): N 4096 x K 14336 38, 43, 54; 14336 x
+// 4096 43, 29, 20; 7168 x 2048 (groups of 64, zero points) 15, 11, 15.
 template <Fmt F, int NT>
 void launch_rows(const uint16_t* x, int M, const WMat& w, const uint16_t* bias, uint16_t* y, hipStream_t st) {
-  const dim3 grid((w.N + 63) / 64, (M + 63) / 64);
-  w4_linear_rows_kernel<F, NT, 4, 8><<<grid, 512, 0, st>>>(x, w, bias, y, M);
+  const unsigned bm = (M + 63) / 64;
+  const auto columns = [&](int rt) { return static_cast<unsigned>((w.N + 16 * rt - 1) / (16 * rt)); };
+  if (columns(1) * bm <= 256) w4_linear_rows_kernel<F, NT, 1, 8><<<dim3(columns(1), bm), 512, 0, st>>>(x, w, bias, y, M);
+  else if (columns(2) * bm <= 256) w4_linear_rows_kernel<F, NT, 2, 8><<<dim3(columns(2), bm), 512, 0, st>>>(x, w, bias, y, M);
+  else w4_linear_rows_kernel<F, NT, 4, 8><<<dim3(columns(4), bm), 512, 0, st>>>(x, w, bias, y, M);
 }
 template <Fmt F>
 hipError_t launch_linear(const uint16_t* x, int M, const WMat& w, const uint16_t* bias, uint16_t* y, hipStream_t st) {
