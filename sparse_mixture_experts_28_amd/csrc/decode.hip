@@ -424,34 +424,42 @@ struct Tickets {
   }
 };
 
-// Shapes of the phase kernels by format and token class (1, up to 16 and up to 64
-// tokens): steps loaded together, tiles of tokens at once (an expert with more
-// makes several jobs), waves that split k in phase 1 (the others take rows of their
-// own), bytes of a wave's activation region.  Two workgroups of eight waves per CU
-// (128 registers a wave, LDS for two).  Measured, phase 1 + phase 2 in us:
+// Shapes of the phase kernels by format, token class (1, up to 16 and up to 64
+// tokens) and, bf16, whether the experts have many tokens each (DENSE: eight and
+// more on average, over 16 tokens): steps loaded together, tiles of tokens at once
+// (an expert with more makes several jobs), tiles of 16 weight rows of a wave,
+// workgroups of eight waves per CU (two: 128 registers a wave, one: 256), bytes of
+// a wave's activation region.  Measured, phase 1 + phase 2 in us:
 //   steps    bf16, one token of the Mixtral shape: 2 + 2 steps 47 + 45, 4 + 4 43 +
 //            46, 4 + 2 a batch ahead 43 + 44, 8 + 8 44 + 50; 4-bit: 2 + 2 steps 22 +
 //            21, 4 + 4 21 + 20
-//   waves    4-bit, 64 tokens of the DeepSeek shape (57 KB of codes to a job and
-//            16 rows): 8 on k 597, 4 536, 2 with four steps 502, 1 579; bf16 lose
-//            by fewer (32 tokens: 8 743, 4 796)
-//   tiles    16 rows of weights to a wave; 32 lose everywhere (registers, and
-//            fewer loads on their way at the end)
 //   WGs      three per CU: 43 + 44 becomes 49 + 53 (one token, Mixtral shape)
-template <Fmt F, int TMAX> struct Shape {
+//   one WG and two row tiles, where a wave multiplies for longer than it loads:
+//     4-bit phase 2 of several tokens: 49 -> 36 (5 tokens, 46 experts, groups of
+//     32), 77 -> 45 (18 tokens, 6 experts, groups of 32), the DeepSeek shape's 64
+//     tokens 1249 -> 1160 for the layer; phase 1 loses (8 tokens, Mixtral shape: 71
+//     -> 81)
+//     DENSE, layer, Mixtral shape: 64 tokens 643 -> 512, 32 tokens 460 -> 437; 45
+//     tokens of 2 + 1 experts 402 -> 242 (tiles for 48 tokens: no weight is read
+//     twice); with few tokens per expert it loses (32 tokens of the DeepSeek
+//     shape 1638 -> 1757), as does float32 (728 -> 818)
+template <Fmt F, int TMAX, bool DENSE> struct Shape {
   static constexpr bool kW = is_w4(F), kMany = TMAX > 16;
-  static constexpr int kRT1 = 1, kRT2 = 1;
-  static constexpr int kU1 = 4, kU2 = kW ? 4 : 2;
+  static constexpr bool kWide2 = DENSE || (kW && TMAX > 1);
+  static constexpr int kRT1 = DENSE ? 2 : 1, kWgs1 = DENSE ? 1 : 2;
+  static constexpr int kRT2 = kWide2 ? 2 : 1, kWgs2 = kWide2 ? 1 : 2;
+  static constexpr int kU1 = 4, kU2 = kW && !(kWide2 && group_shift(F) == 5) ? 4 : 2;
   static constexpr bool kAhead2 = !kW && !kMany;
-  static constexpr int kSplit1 = kW && kMany ? 2 : 8;
-  static constexpr int kNT1 = !kMany || kW ? 1 : 2;
-  static constexpr int kNT2 = kW ? 1 : F == Fmt::kF32 ? kNT1 : TMAX == 1 ? 1 : TMAX == 16 ? 2 : 3;
+  static constexpr int kNT1 = DENSE ? 3 : !kMany || kW ? 1 : 2;
+  static constexpr int kNT2 = DENSE ? 6 : kW ? 1 : F == Fmt::kF32 ? kNT1 : TMAX == 1 ? 1 : TMAX == 16 ? 2 : 3;
   static constexpr int kRows1 = TMAX == 1 ? 1 : 16 * kNT1, kRows2 = TMAX == 1 ? (F == Fmt::kF32 ? 1 : 2) : 16 * kNT2;
-  static constexpr int kRows = kRows1 > kRows2 ? kRows1 : kRows2;   // most rows staged
   static constexpr int kStep = kW ? 256 : 64;
-  static constexpr int kStage = (TMAX == 1 ? (kW ? 2048 : 1024) : kRows * (kStep + 16)) + 32 + kStageZero;
+  static constexpr int stage(int rows) {
+    return (TMAX == 1 ? (kW ? 2048 : 1024) : rows * (kStep + 16)) + 32 + kStageZero;
+  }
+  static constexpr int kStage1 = stage(kRows1) + (DENSE ? 2048 : 0);
+  static constexpr int kStage2 = stage(kRows2) + (kWide2 && !DENSE ? 4352 : 0);
 };
-constexpr int kWgs = 2;
 
 // a segment's products for one tile of tokens or for all NT (the others then
 // hold rows whose sums nobody reads)
@@ -476,20 +484,20 @@ __device__ __forceinline__ void run_tiles(St& st, floatx4 (&acc)[NT][RT], __amdg
 }
 
 // ------------------------------------------------------------------ phase 1 --
-// One item: a job and hidden units, 16 RT for each group of KS waves.  The job's
+// One item: a job and hidden units, 16 for each group of KS waves.  The job's
 // tokens are the activation rows, NT tiles of 16; a group's waves split k and add
 // their sums in LDS in wave order.  The next item's first loads are issued before this one's sums, biases,
 // activations and stores.
-template <Fmt F, int TMAX>
-__global__ __launch_bounds__(kThreads, 4) void decode_phase1_kernel(DecodeArgs a) {
-  using Sh = Shape<F, TMAX>;
+template <Fmt F, int TMAX, bool DENSE>
+__global__ __launch_bounds__(kThreads, (2 * Shape<F, TMAX, DENSE>::kWgs1)) void decode_phase1_kernel(DecodeArgs a) {
+  using Sh = Shape<F, TMAX, DENSE>;
   constexpr bool kBf = F != Fmt::kF32;
-  constexpr int NT = Sh::kNT1, RT = Sh::kRT1, U = Sh::kU1, KS = Sh::kSplit1;
-  constexpr int kN = 16 * RT * (kWaves / KS);
-  using St = Stream<F, RT, U, false, true, Sh::kRows, Sh::kStage>;
+  constexpr int NT = Sh::kNT1, RT = Sh::kRT1, U = Sh::kU1;
+  const int KS = a.ksplit, kN = 16 * RT * (kWaves / KS);   // waves that split k; hidden units of an item
+  using St = Stream<F, RT, U, false, true, Sh::kRows1, Sh::kStage1>;
   __shared__ Routing r;
   __shared__ float red[NT * RT * kWaves * 256];
-  __shared__ __attribute__((aligned(16))) char stages[kWaves][Sh::kStage];
+  __shared__ __attribute__((aligned(16))) char stages[kWaves][Sh::kStage1];
   __shared__ int next[2];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   char* stage = stages[wave];
@@ -539,14 +547,13 @@ __global__ __launch_bounds__(kThreads, 4) void decode_phase1_kernel(DecodeArgs a
     item = tk.take();
     if (item < items) begin(item);
     for (int i = threadIdx.x; i < tl * 16 * kN; i += kThreads) {
-      // result (row p of the job's tokens, hidden unit n): row tile rt of the waves
-      // wg KS .., lane (n, p / 4 % 4), register p % 4
-      const int rt16 = i >> 8, j = rt16 / (kN / 16), wr = rt16 % (kN / 16), wg = wr / RT, rt = wr % RT;
+      // result (row p of the job's tokens, hidden unit n): waves wg KS .., lane (n, p /
+      // 4 % 4), register p % 4
+      const int rt16 = i >> 8, j = rt16 / (kN / 16), wr = rt16 - j * (kN / 16), wg = wr / RT, rt = wr % RT;
       const int n = cn0 + wr * 16 + (i & 15), pr = (i >> 4) & 15, p = j * 16 + pr;
       if (p >= crows || n >= a.h) continue;
       const float* sum = red + (((j * RT + rt) * kWaves + wg * KS) * 64 + (pr >> 2) * 16 + (i & 15)) * 4 + (pr & 3);
       float v = 0.f;
-#pragma unroll
       for (int w = 0; w < KS; ++w) v += sum[w * 256];
       if (a.b1 != nullptr) v += load1<kBf>(a.b1, static_cast<size_t>(ce) * a.h + n);
       v = a.act == MOE_ACT_SILU ? v / (1.f + expf(-v)) : 0.5f * v * (1.f + erff(v * 0.70710678118654752440f));
@@ -592,16 +599,16 @@ __device__ __forceinline__ void write_out(const DecodeArgs& a, const Routing& r,
 // only.  Each wave adds them to a table of its own in LDS, [T][16 RT]; the tables
 // are added in wave order at the end.  Loads run ahead as in phase 1: the next
 // job's before a job's sums, the next item's before an item's.
-template <Fmt F, int TMAX>
-__global__ __launch_bounds__(kThreads, 4) void decode_phase2_kernel(DecodeArgs a) {
-  using Sh = Shape<F, TMAX>;
+template <Fmt F, int TMAX, bool DENSE>
+__global__ __launch_bounds__(kThreads, (2 * Shape<F, TMAX, DENSE>::kWgs2)) void decode_phase2_kernel(DecodeArgs a) {
+  using Sh = Shape<F, TMAX, DENSE>;
   constexpr bool kBf = F != Fmt::kF32;
   constexpr int kTok = kBf ? 8 : 16;
   constexpr int NT = Sh::kNT2, RT = Sh::kRT2, U = Sh::kU2, kN = 16 * RT;
-  using St = Stream<F, RT, U, Sh::kAhead2, true, Sh::kRows, Sh::kStage>;
+  using St = Stream<F, RT, U, Sh::kAhead2, true, Sh::kRows2, Sh::kStage2>;
   __shared__ Routing r;
   __shared__ float tab[kWaves][TMAX * kN];
-  __shared__ __attribute__((aligned(16))) char stages[kWaves][Sh::kStage];
+  __shared__ __attribute__((aligned(16))) char stages[kWaves][Sh::kStage2];
   __shared__ int next[2];
   __shared__ int flag;
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
@@ -728,23 +735,23 @@ __global__ __launch_bounds__(kThreads, 4) void decode_phase2_kernel(DecodeArgs a
 }
 
 // F: the format without zero points, Z: with them (the same where there are none)
-template <Fmt F, Fmt Z, int TMAX>
+template <Fmt F, Fmt Z, int TMAX, bool DENSE>
 hipError_t launch_phases(const DecodeArgs& a, hipStream_t st) {
-  const int grid = device_cu_count() * kWgs;
+  const int grid = device_cu_count() * Shape<F, TMAX, DENSE>::kWgs1, grid2 = device_cu_count() * Shape<F, TMAX, DENSE>::kWgs2;
   if (a.T > kWaves) decode_select_kernel<<<a.T, 64, 0, st>>>(a);
-  if (a.W1.z != nullptr) decode_phase1_kernel<Z, TMAX><<<grid, kThreads, 0, st>>>(a);
-  else decode_phase1_kernel<F, TMAX><<<grid, kThreads, 0, st>>>(a);
+  if (a.W1.z != nullptr) decode_phase1_kernel<Z, TMAX, DENSE><<<grid, kThreads, 0, st>>>(a);
+  else decode_phase1_kernel<F, TMAX, DENSE><<<grid, kThreads, 0, st>>>(a);
   const hipError_t e = hipGetLastError();   // of either launch: a failed one is remembered
   if (e != hipSuccess) return e;
-  if (a.W2.z != nullptr) decode_phase2_kernel<Z, TMAX><<<grid, kThreads, 0, st>>>(a);
-  else decode_phase2_kernel<F, TMAX><<<grid, kThreads, 0, st>>>(a);
+  if (a.W2.z != nullptr) decode_phase2_kernel<Z, TMAX, DENSE><<<grid2, kThreads, 0, st>>>(a);
+  else decode_phase2_kernel<F, TMAX, DENSE><<<grid2, kThreads, 0, st>>>(a);
   return hipGetLastError();
 }
 template <Fmt F, Fmt Z>
 hipError_t launch_phases(const DecodeArgs& a, hipStream_t st) {
-  if (a.T == 1) return launch_phases<F, Z, 1>(a, st);
-  if (a.T <= 16) return launch_phases<F, Z, 16>(a, st);
-  return launch_phases<F, Z, kMaxT>(a, st);
+  if (a.T == 1) return launch_phases<F, Z, 1, false>(a, st);
+  if (a.T <= 16) return launch_phases<F, Z, 16, false>(a, st);
+  return launch_phases<F, Z, kMaxT, false>(a, st);
 }
 
 template <bool BF16>
@@ -765,19 +772,32 @@ void launch_logits(const DecodeArgs& a, hipStream_t st) {
 //            more (a second round that is mostly empty is the worst of both); of
 //            32 KB at least, 64 at most
 //   dynamic  2 MB or more to read per workgroup and phase
+//   ksplit   phase 1: waves that split k, the others take rows of their own: all
+//            eight, but no more than there are batches, and fewer while a wave has
+//            less than four batches and the items still make two rounds (4-bit, 64
+//            tokens of the DeepSeek shape, 14 batches: 8 waves 597 us, 4 536, 2 502;
+//            4-bit, d = 1024, two batches: 8 waves leave six without work)
+//   dense    bf16: over 16 tokens, eight and more to an expert
 DecodePlan decode_plan(int T, int d, int h, int E, int k, int S, int fmt) {
   const double used = E * (1.0 - std::pow(1.0 - static_cast<double>(k) / E, T)) + S;
   const double elem = fmt == kDecodeF32 ? 4.0 : fmt == kDecodeBf16 ? 2.0 : 0.5;
-  const int tiles = (d + 15) / 16;
-  const double tile_bytes = used * 16 * h * elem;
-  const int slots = 256 * kWgs;
+  const bool dense = fmt == kDecodeBf16 && T > 16 && T * k >= 8 * E;
+  const int rt1 = dense ? 2 : 1, rt = dense || (fmt == kDecodeW4 && T > 1) ? 2 : 1;   // row tiles of a wave
+  const int tiles = (d + 16 * rt - 1) / (16 * rt);
+  const double tile_bytes = used * 16 * rt * h * elem;
+  const int slots1 = 512 / rt1, slots = 512 / rt;   // workgroups of phase 1 and 2
   int sp = tiles < slots ? slots / tiles : 1;
   const double by_size = tile_bytes / (1 << 20);
   if (by_size >= 3.0 * sp) sp = by_size < 64.0 ? static_cast<int>(by_size) : 64;
   const double most = tile_bytes / 32768;
   if (sp > most) sp = most < 1.0 ? 1 : static_cast<int>(most);
   if (sp > 64) sp = 64;
-  return DecodePlan{sp, used * d * h * elem >= (2 << 20) * static_cast<double>(slots) ? 1 : 0};
+  const int step = fmt == kDecodeF32 ? 16 : fmt == kDecodeBf16 ? 32 : 128;
+  const int nb = ((d + step - 1) / step + 3) / 4;   // batches of four steps
+  int ks = kWaves;
+  while (ks > 1 && ks > nb) ks >>= 1;
+  while (ks > 1 && nb / ks < 4 && used * h / (16. * rt1 * (2 * kWaves / ks)) >= 2.0 * slots1) ks >>= 1;
+  return DecodePlan{sp, used * d * h * elem >= (2 << 20) * static_cast<double>(slots1) ? 1 : 0, ks, dense ? 1 : 0};
 }
 
 hipError_t launch_decode(const DecodeArgs& a, hipStream_t st) {
@@ -786,6 +806,7 @@ hipError_t launch_decode(const DecodeArgs& a, hipStream_t st) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   if (a.fmt == kDecodeF32) return launch_phases<Fmt::kF32, Fmt::kF32>(a, st);
+  if (a.fmt == kDecodeBf16 && a.dense) return launch_phases<Fmt::kBf16, Fmt::kBf16, kMaxT, true>(a, st);
   if (a.fmt == kDecodeBf16) return launch_phases<Fmt::kBf16, Fmt::kBf16>(a, st);
   if (a.W1.gshift == 5) return launch_phases<Fmt::kW4g32, Fmt::kW4g32z>(a, st);
   if (a.W1.gshift == 6) return launch_phases<Fmt::kW4g64, Fmt::kW4g64z>(a, st);

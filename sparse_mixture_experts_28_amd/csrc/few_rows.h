@@ -56,8 +56,7 @@ struct WRows {
   uint32_t pair, tile;
   __amdgpu_buffer_rsrc_t s, z;   // 4-bit: the rows' scales and zero points
   uint32_t srow, stile;          // 4-bit: first scale of the lane's row, scales of 16 rows
-  bool wide;                     // 4-bit: every four scales from a multiple of four on start at a multiple of
-                                 // four bytes, and so do their zero points
+  bool wide;                     // 4-bit: no word of a batch's scales (zero points) is cut by the array's end
 };
 
 template <Fmt F, int RT>
@@ -74,12 +73,15 @@ __device__ __forceinline__ WRows rows_of(const WMat& m, long long mat, int n0, i
     o.voff[1] = o.voff[0] + 64u;
     o.pair = 128u;
     o.tile = 16u * pitch;
-    o.s = make_rsrc(m.s + row0 * ng, static_cast<uint32_t>(left) * ng * 2u);
+    // the rest of the array, as far as 32 bits go: a batch's load may reach past
+    // the rows' scales, and a word cut by the end of the range would read as zero
+    const long long rest = (m.scales - row0 * ng) < (1ll << 28) ? m.scales - row0 * ng : 1ll << 28;
+    o.s = make_rsrc(m.s + row0 * ng, static_cast<uint32_t>(rest) * 2u);
     o.z = o.s;
-    if (m.z != nullptr) o.z = make_rsrc(m.z + row0 * ng, static_cast<uint32_t>(left) * ng);
+    if (has_zeros(F)) o.z = make_rsrc(m.z + row0 * ng, static_cast<uint32_t>(rest));
+    o.wide = m.whole || static_cast<long long>(16 * RT) * ng + 64 <= rest;
     o.srow = static_cast<uint32_t>(r) * ng;
     o.stile = 16u * ng;
-    o.wide = m.wide != 0;
   } else {
     constexpr uint32_t eb = F == Fmt::kF32 ? 4 : 2;
     const uint32_t pitch = static_cast<uint32_t>(m.K) * eb;
@@ -179,8 +181,10 @@ template <Fmt F> constexpr int mfma_k(int i) {
 // ---------------------------------------------------------------- a batch --
 // The weights of U steps from step s0 (a multiple of U) on, k < kend.  4-bit:
 // with the batch's scales, two to a word, and zero points, four to a word, in
-// every lane of their row; one load brings as many as it can where the rows
-// allow it (one 2-byte load per step cost 3 to 5 us of a 23 us phase).
+// every lane of their row, by loads as wide as they come, at any 2-byte (zero
+// points: 1-byte) address (one 2-byte load per step cost 3 to 5 us of a 23 us
+// phase); one by one only where such a load could leave the array, in its last
+// rows.
 template <Fmt F, int RT, int U> struct WBatch {
   static constexpr int kS = is_w4(F) ? U << (7 - group_shift(F)) : 2;   // scales of a row and batch
   static_assert(kS >= 2 && kS <= 16, "whole words of scales");

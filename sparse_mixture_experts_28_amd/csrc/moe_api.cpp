@@ -300,9 +300,10 @@ namespace {
 
 int group_shift(int32_t group) { return group == 32 ? 5 : group == 64 ? 6 : group == 128 ? 7 : -1; }
 
-WMat w4_matrix(const uint8_t* codes, const void* scales, const uint8_t* zeros, int N, int K, int gs) {
-  const int wide = ((K >> gs) % 4 == 0 && aligned(scales, 4) && (zeros == nullptr || aligned(zeros, 4))) ? 1 : 0;
-  return WMat{reinterpret_cast<const char*>(codes), static_cast<const uint16_t*>(scales), zeros, N, K, 0, gs, wide};
+WMat w4_matrices(int n, const uint8_t* codes, const void* scales, const uint8_t* zeros, int N, int K, int gs) {
+  const bool whole = (K >> gs) % 4 == 0 && aligned(scales, 4) && (zeros == nullptr || aligned(zeros, 4));
+  return WMat{reinterpret_cast<const char*>(codes), static_cast<const uint16_t*>(scales), zeros, N, K, 0, gs,
+              static_cast<long long>(n) * N * (K >> gs), whole ? 1 : 0};
 }
 
 // The few-row kernels address the activations, the hidden rows and 16 weight
@@ -368,6 +369,8 @@ moe_status_t forward_decode(DecodeArgs a, const moe_launch_t* launch) {
   a.ncounter = L.ncounter;
   a.split = L.plan.split;
   a.dynamic = L.plan.dynamic;
+  a.ksplit = L.plan.ksplit;
+  a.dense = L.plan.dense;
   (void)hipGetLastError();
   const hipError_t e = launch_decode(a, launch->stream);
   if (e != hipSuccess) {
@@ -592,8 +595,8 @@ moe_status_t moe_forward_decode_w4(const void* x, const void* W_g, const uint8_t
   a.x = x; a.W_g = W_g; a.b1 = b1; a.b2 = b2; a.out = out; a.topk_idx = topk_idx; a.topk_w = topk_w;
   a.E = E; a.k = k; a.S = n_shared;
   a.fmt = kDecodeW4;
-  a.W1 = w4_matrix(W1, W1_scales, W1_zeros, h, d, gs);
-  a.W2 = w4_matrix(W2, W2_scales, W2_zeros, d, h, gs);
+  a.W1 = w4_matrices(E + n_shared, W1, W1_scales, W1_zeros, h, d, gs);
+  a.W2 = w4_matrices(E + n_shared, W2, W2_scales, W2_zeros, d, h, gs);
   return forward_decode(a, launch);
 }
 
@@ -633,7 +636,7 @@ moe_status_t moe_linear_w4(const void* x, int32_t M, const uint8_t* codes, const
   if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 2) || !aligned(y, 2) || (bias && !aligned(bias, 2)))
     return MOE_ERR_UNSUPPORTED;
   (void)hipGetLastError();
-  return w4_status(launch_w4_linear(static_cast<const uint16_t*>(x), M, w4_matrix(codes, scales, zeros, N, K, gs),
+  return w4_status(launch_w4_linear(static_cast<const uint16_t*>(x), M, w4_matrices(1, codes, scales, zeros, N, K, gs),
                                     static_cast<const uint16_t*>(bias), static_cast<uint16_t*>(y), stream),
                    "4-bit Linear");
 }

@@ -328,7 +328,8 @@ struct WMat {
   int N, K;
   int packed;          // bf16: tile-packed layout
   int gshift;          // 4-bit: log2 of the elements per scale
-  int wide;            // 4-bit: K / group a multiple of four, scales and zero points 4-byte aligned
+  long long scales;    // 4-bit: scales of all matrices
+  int whole;           // 4-bit: K / group a multiple of four, scales and zero points 4-byte aligned
 };
 enum DecodeFmt { kDecodeF32 = 0, kDecodeBf16 = 1, kDecodeW4 = 2 };
 struct DecodeArgs {
@@ -353,9 +354,11 @@ struct DecodeArgs {
   int fmt;
   int split;            // shares of phase 2's sum per tile of output columns
   int dynamic;          // items handed out by a counter
+  int dense;            // experts have many tokens each
+  int ksplit;           // waves that split k in phase 1 (a power of two)
 };
 struct DecodePlan {
-  int split, dynamic;
+  int split, dynamic, ksplit, dense;
 };
 DecodePlan decode_plan(int T, int d, int h, int E, int k, int S, int fmt);
 hipError_t launch_decode(const DecodeArgs& a, hipStream_t st);

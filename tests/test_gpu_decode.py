@@ -73,7 +73,8 @@ SHAPES = [
     (1, 8, 8, 1, 1, 0), (1, 64, 128, 4, 2, 0), (2, 40, 24, 5, 5, 0), (7, 264, 72, 8, 2, 1), (8, 256, 512, 16, 4, 0),
     (9, 512, 256, 16, 2, 2), (16, 136, 2056, 64, 8, 0), (17, 1024, 96, 3, 1, 0), (33, 72, 520, 256, 8, 1),
     (63, 32, 128, 4, 2, 0), (64, 512, 1024, 8, 2, 8), (64, 128, 64, 256, 8, 0), (3, 4096, 520, 8, 2, 0),
-    (5, 16, 8192, 8, 2, 0), (64, 24, 4104, 2, 1, 1),
+    (5, 16, 8192, 8, 2, 0), (64, 24, 4104, 2, 1, 1), (17, 328, 1064, 2, 1, 1), (48, 72, 4104, 1, 1, 1),
+    (49, 1032, 488, 3, 2, 0),
 ]
 
 
@@ -84,7 +85,8 @@ def test_shapes(T, d, h, E, k, S, dtype):
     check(p, run(on_gpu(p)))
 
 
-@pytest.mark.parametrize("T,d,h,E,k,S", [(1, 256, 256, 4, 2, 0), (13, 512, 768, 8, 2, 1), (40, 256, 1024, 16, 4, 0)])
+@pytest.mark.parametrize("T,d,h,E,k,S", [(1, 256, 256, 4, 2, 0), (13, 512, 768, 8, 2, 1), (40, 256, 1024, 16, 4, 0),
+                                           (64, 512, 768, 4, 2, 1)])
 def test_packed_weights_give_the_same_bits(T, d, h, E, k, S):
     p = make(T, d, h, E, k, S, seed=3)
     q = on_gpu(p)
@@ -96,7 +98,8 @@ def test_packed_weights_give_the_same_bits(T, d, h, E, k, S):
 @pytest.mark.parametrize("zeros", [False, True])
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("T,dg,hg,E,k,S", [(1, 1, 1, 1, 1, 0), (1, 5, 9, 8, 2, 0), (6, 3, 4, 4, 3, 1),
-                                           (12, 7, 2, 16, 2, 0), (33, 2, 11, 64, 8, 1), (64, 4, 3, 8, 2, 0)])
+                                           (12, 7, 2, 16, 2, 0), (33, 2, 11, 64, 8, 1), (64, 4, 3, 8, 2, 0),
+                                           (3, 33, 67, 4, 2, 1)])
 def test_w4(T, dg, hg, E, k, S, group, zeros):
     p = make(T, dg * group, hg * group, E, k, S, act="gelu" if T % 2 else "silu", bias=E > 4, b_g=T > 6, seed=T + group,
              group=group, zeros=zeros)
