@@ -315,6 +315,7 @@ moe_status_t moe_forward_noalloc(const void* x, const void* W_g, const void* W1,
  *           (else MOE_ERR_UNSUPPORTED).  The stream must belong to the calling
  *           thread's current device.  Calls that may overlap, graph replays among
  *           them, need distinct workspaces; the contents need not be initialised.
+ *           Outputs and workspace must not overlap inputs or one another.
  * MOE_ERR_UNSUPPORTED also for T > MOE_MAX_DECODE_TOKENS, d or h above 2^20, and
  * T (k + S) h above 2^28; other errors as for moe_forward. */
 size_t moe_workspace_bytes_decode(int32_t T, int32_t d, int32_t h, int32_t E, int32_t k, int32_t n_shared,
@@ -345,12 +346,13 @@ moe_status_t moe_forward_decode(const void* x, const void* W_g, const void* W1, 
  * moe_linear_w4: y[m, n] = sum_j x[m, j] w[n, j] + bias[n] for M rows of bf16 x
  * [M, K] (16-byte aligned), y [M, N] and bias [N] (or NULL) bf16; the sums in
  * float32 on the unrounded s (q - z), y rounded once.  Made for a few rows: the
- * codes are read once per 64 rows.  K at most 2^20, M at most 2^21 (else
- * MOE_ERR_UNSUPPORTED).  An infinite x gives NaN in its row.
+ * codes are read once per 64 rows.  K at most 2^20, M at most 2^21, N at most
+ * 2^26 (else MOE_ERR_UNSUPPORTED).  An infinite x gives NaN in its row.
  *
- * Each enqueues on `stream` and returns MOE_OK, or MOE_ERR_ARG (a NULL required
- * pointer, a size below 1), MOE_ERR_UNSUPPORTED (another group, cols or K not a
- * multiple of it, alignment) or MOE_ERR_HIP. */
+ * Each enqueues on `stream` (of the calling thread's current device) and returns
+ * MOE_OK, or MOE_ERR_ARG (a NULL required pointer, a size below 1),
+ * MOE_ERR_UNSUPPORTED (another group, cols or K not a multiple of it, alignment) or
+ * MOE_ERR_HIP.  Outputs must not overlap inputs. */
 moe_status_t moe_quantize_w4(const void* src, int32_t rows, int32_t cols, int32_t group, uint8_t* codes,
                              void* scales, uint8_t* zeros, hipStream_t stream);
 moe_status_t moe_dequantize_w4(const uint8_t* codes, const void* scales, const uint8_t* zeros, int32_t rows,

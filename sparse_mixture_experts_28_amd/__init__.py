@@ -346,6 +346,13 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _int32(n: int) -> int:
+    """n as the C interface takes it; ctypes would cut it to 32 bits without a word."""
+    if not -1 << 31 <= n < 1 << 31:
+        raise ValueError(f"{n} is out of range")
+    return n
+
+
 def _decode(fn, x, W_g, weights, b1, W1, b2, k, S, b_g, b_sel, activation, packed, workspace, nbytes, extra=()):
     """Checks shared by the few-token layers, outputs, workspace and the call.
     ``weights``: the weight arguments in the order of the C call; ``extra``:
@@ -360,6 +367,8 @@ def _decode(fn, x, W_g, weights, b1, W1, b2, k, S, b_g, b_sel, activation, packe
     if gpu < 0 or not x.is_contiguous() or not _on(W_g, gpu, dt) or (b1 is not None and not _on(b1, gpu, dt)) or \
             (b2 is not None and not _on(b2, gpu, dt)):
         raise ValueError("x, W_g and the biases must be contiguous tensors of one dtype on one GPU")
+    if not (0 <= k < 1 << 31 and 0 <= S < 1 << 31):
+        raise ValueError("k or n_shared out of range")
     if W_g.shape != (E, d) or (b1 is not None and b1.shape != (E + S, h)) or \
             (b2 is not None and b2.shape != (E + S, d)):
         raise ValueError("inconsistent shapes")
@@ -442,7 +451,7 @@ def quantize_w4(w, group: int = 128, zero_points: bool = False):
     codes = torch.empty((*lead, K // 2), dtype=torch.uint8, device=dev)
     scales = torch.empty((*lead, K // group), dtype=torch.bfloat16, device=dev)
     zeros = torch.empty((*lead, K // group), dtype=torch.uint8, device=dev) if zero_points else None
-    _call(gpu, LIB.moe_quantize_w4, w.data_ptr(), w.numel() // K, K, group, codes.data_ptr(), scales.data_ptr(),
+    _call(gpu, LIB.moe_quantize_w4, w.data_ptr(), _int32(w.numel() // K), _int32(K), group, codes.data_ptr(), scales.data_ptr(),
           _ptr(zeros))
     return codes, scales, zeros
 
@@ -457,8 +466,8 @@ def dequantize_w4(codes, scales, zeros=None):
     group = _w4_group(codes, scales, zeros, gpu)
     *lead, half = codes.shape
     out = torch.empty((*lead, 2 * half), dtype=torch.bfloat16, device=codes.device)
-    _call(gpu, LIB.moe_dequantize_w4, codes.data_ptr(), scales.data_ptr(), _ptr(zeros), codes.numel() // half, 2 * half,
-          group, out.data_ptr())
+    _call(gpu, LIB.moe_dequantize_w4, codes.data_ptr(), scales.data_ptr(), _ptr(zeros), _int32(codes.numel() // half),
+          _int32(2 * half), group, out.data_ptr())
     return out
 
 
@@ -473,8 +482,8 @@ def linear_w4(x, codes, scales, zeros=None, bias=None):
     if codes.dim() != 2 or codes.numel() == 0:
         raise ValueError("linear_w4 takes non-empty codes [N, K/2]")
     group = _w4_group(codes, scales, zeros, gpu)
-    M, K = x.shape
-    N, half = codes.shape
+    M, K = map(_int32, x.shape)
+    N, half = map(_int32, codes.shape)
     if 2 * half != K:
         raise ValueError("inconsistent shapes of x and the 4-bit weight")
     if bias is not None and (not _on(bias, gpu, torch.bfloat16) or bias.shape != (N,)):

@@ -20,7 +20,6 @@
 namespace moe {
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
 constexpr uint32_t kOut = 0x7ffffff0u;   // an offset past every range used here: the load returns zero
 

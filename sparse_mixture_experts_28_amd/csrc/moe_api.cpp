@@ -632,7 +632,8 @@ moe_status_t moe_linear_w4(const void* x, int32_t M, const uint8_t* codes, const
   using namespace moe;
   if (!x || !codes || !scales || !y || M < 1 || N < 1 || K < 1) return MOE_ERR_ARG;
   const int gs = group_shift(group);
-  if (gs < 0 || K % group != 0 || K > (1 << 20) || M > (1 << 21)) return MOE_ERR_UNSUPPORTED;
+  // M: rows of 64 in a grid's second dimension; N: 32 threads a column in its first
+  if (gs < 0 || K % group != 0 || K > (1 << 20) || M > (1 << 21) || N > (1 << 26)) return MOE_ERR_UNSUPPORTED;
   if (!aligned(x, 16) || !aligned(codes, 16) || !aligned(scales, 2) || !aligned(y, 2) || (bias && !aligned(bias, 2)))
     return MOE_ERR_UNSUPPORTED;
   (void)hipGetLastError();

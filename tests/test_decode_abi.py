@@ -122,4 +122,4 @@ def test_w4_calls():
     assert li(K=96) == moe.MOE_ERR_UNSUPPORTED and li(K=(1 << 20) + 64) == moe.MOE_ERR_UNSUPPORTED
     assert q(src=FAKE + 2) == moe.MOE_ERR_UNSUPPORTED and d(dst=FAKE + 2) == moe.MOE_ERR_UNSUPPORTED
     assert li(x=FAKE + 8) == moe.MOE_ERR_UNSUPPORTED and li(bias=FAKE + 1) == moe.MOE_ERR_UNSUPPORTED
-    assert li(M=(1 << 21) + 1) == moe.MOE_ERR_UNSUPPORTED
+    assert li(M=(1 << 21) + 1) == moe.MOE_ERR_UNSUPPORTED and li(N=(1 << 26) + 1) == moe.MOE_ERR_UNSUPPORTED

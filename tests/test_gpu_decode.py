@@ -214,6 +214,30 @@ def test_graph_replays_and_two_streams(kw):
             assert torch.equal(a.out, b.out) and torch.equal(a.topk_idx, b.topk_idx)
 
 
+def test_refusals():
+    import sparse_mixture_experts_28_amd as moe
+    host = make(4, 64, 96, 4, 2, 1, seed=2)
+    p, q = on_gpu(host), on_gpu(make(4, 64, 96, 4, 2, 1, seed=2, group=32, zeros=True))
+    small = torch.zeros(256, dtype=torch.uint8, device=DEV)
+    long = torch.zeros(65, 64, dtype=torch.bfloat16, device=DEV)
+    odd = torch.zeros(1 << 20, dtype=torch.uint8, device=DEV)[1:]
+    big = lambda t: torch.zeros(*t.shape[:-1], 2 * t.shape[-1], dtype=t.dtype, device=DEV)[..., ::2]
+    common = [dict(x=p["x"].float()), dict(x=p["x"].cpu()), dict(x=long), dict(x=long[:0]), dict(x=big(p["x"])),
+              dict(W_g=p["W_g"].float()), dict(W_g=p["W_g"][:3]), dict(W_g=p["W_g"].cpu()), dict(k=0), dict(k=5),
+              dict(k=(1 << 32) + 2), dict(S=0), dict(S=-1), dict(b1=p["b1"][:4]), dict(b2=p["b2"].float()),
+              dict(b_g=p["b1"][0, :4]), dict(b_sel=torch.zeros(5, device=DEV)), dict(act="relu"),
+              dict(workspace=small), dict(workspace=torch.zeros(1 << 20, dtype=torch.uint8)), dict(workspace=odd)]
+    wide = [dict(W1=p["W1"].float()), dict(W1=p["W1"].cpu()), dict(W2=p["W2"][:4]), dict(W1=p["W1"].transpose(1, 2)),
+            dict(packed=True)]
+    four = [dict(W1s=q["W1s"].float()), dict(W1=q["W1"][..., ::2]), dict(W1z=q["W1z"][:4]), dict(W2s=q["W2s"][..., :1]),
+            dict(W1=q["W1"].cpu()), dict(W2z=q["W2z"].to(torch.int8))]
+    for base, bad in [(p, b) for b in common + wide] + [(q, b) for b in common + four]:
+        kw = {n: bad[n] for n in ("packed", "workspace") if n in bad}
+        with pytest.raises((ValueError, RuntimeError)):
+            run(dict(base, **{n: v for n, v in bad.items() if n not in kw}), **kw)
+    check(host, run(p, workspace=torch.zeros(1 << 20, dtype=torch.uint8, device=DEV)))   # and the calls before left no error
+
+
 def test_as_a_server_would_use_them():
     """A prompt through the grouped layer, its continuation token by token through the few-token layer, and both again
     on 4-bit weights read back for the prompt: routing agrees, and the outputs agree within the two paths' roundings."""
