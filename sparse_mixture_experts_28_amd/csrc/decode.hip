@@ -456,7 +456,7 @@ template <Fmt F, int TMAX, bool DENSE> struct Shape {
   static constexpr int kRows1 = TMAX == 1 ? 1 : 16 * kNT1, kRows2 = TMAX == 1 ? (F == Fmt::kF32 ? 1 : 2) : 16 * kNT2;
   static constexpr int kStep = kW ? 256 : 64;
   static constexpr int stage(int rows) {
-    return (TMAX == 1 ? (kW ? 2048 : 1024) : rows * (kStep + 16)) + 32 + kStageZero;
+    return (TMAX == 1 ? (kW ? 2048 : 1024) : rows * (kStep + 16)) + 32 + stage_zero(F);
   }
   static constexpr int kStage1 = stage(kRows1) + (DENSE ? 2048 : 0);
   static constexpr int kStage2 = stage(kRows2) + (kWide2 && !DENSE ? 4352 : 0);
@@ -464,8 +464,8 @@ template <Fmt F, int TMAX, bool DENSE> struct Shape {
 
 // a segment's products for one tile of tokens or for all NT (the others then
 // hold rows whose sums nobody reads)
-template <int NT, int RT, typename St, typename SlotOff>
-__device__ __forceinline__ void run_tiles(St& st, floatx4 (&acc)[NT][RT], __amdgpu_buffer_rsrc_t a, SlotOff soff,
+template <int NT, int RT, typename St>
+__device__ __forceinline__ void run_tiles(St& st, floatx4 (&acc)[NT][RT], __amdgpu_buffer_rsrc_t a,
                                           const int (&rslot)[NT], int tl, char* stage, int lane) {
 #pragma unroll
   for (int j = 0; j < NT; ++j)
@@ -476,11 +476,11 @@ __device__ __forceinline__ void run_tiles(St& st, floatx4 (&acc)[NT][RT], __amdg
     const int rs[1] = {rslot[0]};
 #pragma unroll
     for (int i = 0; i < RT; ++i) one[0][i] = acc[0][i];
-    st.run(one, a, soff, rs, stage, lane);
+    st.run(one, a, rs, stage, lane);
 #pragma unroll
     for (int i = 0; i < RT; ++i) acc[0][i] = one[0][i];
   } else {
-    st.run(acc, a, soff, rslot, stage, lane);
+    st.run(acc, a, rslot, stage, lane);
   }
 }
 
@@ -534,7 +534,7 @@ __global__ __launch_bounds__(kThreads, (2 * Shape<F, TMAX, DENSE>::kWgs1)) void 
 #pragma unroll
     for (int j = 0; j < NT; ++j) rslot[j] = min(j * 16 + (lane & 15), rows - 1);
     floatx4 acc[NT][RT];
-    run_tiles(st, acc, xr, soff, rslot, tl, stage, lane);
+    run_tiles(st, acc, xr, rslot, tl, stage, lane);
 #pragma unroll
     for (int j = 0; j < NT; ++j)
       if (j < tl) {
@@ -680,7 +680,7 @@ __global__ __launch_bounds__(kThreads, (2 * Shape<F, TMAX, DENSE>::kWgs2)) void 
         if (kBf && (lane & 8)) rslot[j] += rows;
       }
       floatx4 acc[NT][RT];
-      run_tiles(st, acc, hr, soff, rslot, tl, stage, lane);
+      run_tiles(st, acc, hr, rslot, tl, stage, lane);
       const int co = o, crows = rows;
       rows = 0;
       if (f < fend) {

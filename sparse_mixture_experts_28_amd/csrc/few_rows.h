@@ -348,15 +348,17 @@ __device__ __forceinline__ void multiply_step(floatx4 (&acc)[NT][RT], const WBat
 // by the lanes that need them, the few rows would take as many load instructions
 // as the weights; staged, a row's bytes are read once, densely.  Slot i of the
 // region holds a chunk of steps of row i, padded by 16 bytes so that neighbouring
-// rows start in different banks; the region's last 16 bytes are zero.
+// rows start in different banks; the region's last stage_zero bytes are zero: what
+// the lanes read for steps past the last.
 //
 // begin() issues the first loads, run() does the rest: called before the work
 // that ends the segment before (sums across waves, activation, stores), begin()
 // keeps the memory busy meanwhile.  kAhead: run() loads a batch ahead of its
 // products too (registers for one more batch).
-constexpr int kStageZero = 16;
+constexpr int stage_zero(Fmt f) { return is_w4(f) ? 2 * mfma_k<Fmt::kW4g32>(3) + 16 : 16; }   // a lane's reads of a step
 
 template <Fmt F, int RT, int U, bool kAhead, bool kOrdered, int SLOTS, int STAGE> struct Stream {
+  static constexpr int kStageZero = stage_zero(F);
   static constexpr int kStep = step_k(F) * act_bytes(F);     // activation bytes of a step and row
   static constexpr int kLoads = (STAGE - kStageZero + 1023) / 1024;
   static constexpr bool kDense = SLOTS * (U * kStep + 16) + kStageZero > STAGE;   // a chunk may be shorter than a batch
@@ -365,21 +367,20 @@ template <Fmt F, int RT, int U, bool kAhead, bool kOrdered, int SLOTS, int STAGE
   WRows wr;
   WBatch<F, RT, U> w;
   u32x4 xv[kLoads];
+  uint32_t xo[kLoads];
   int s0, s1, kend, slots, cs;
 
   static __device__ __forceinline__ void clear(char* stage, int lane) {
     if (lane < kStageZero / 4) reinterpret_cast<int*>(stage + STAGE - kStageZero)[lane] = 0;
   }
 
-  // the chunk of activations from step c0 on: slot i at soff(i) bytes of a
-  template <typename SlotOff>
-  __device__ __forceinline__ void load_x(__amdgpu_buffer_rsrc_t a, SlotOff soff, int c0, int lane) {
+  // the chunk of activations from step c0 on: slot i at xo[..] = soff(i) + .. bytes of a
+  __device__ __forceinline__ void load_x(__amdgpu_buffer_rsrc_t a, int c0, int lane) {
     constexpr int kUnits = kStep == 64 ? 2 : 4;              // log2 of a step's 16-byte units
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
-      const int unit = i * 64 + lane, slot = unit >> (cs + kUnits);
-      const int at = c0 * kStep + ((unit & ((1 << (cs + kUnits)) - 1)) << 4);
-      xv[i] = load16(a, slot < slots && at < kend * act_bytes(F) ? soff(slot) + at : kOut, 0);
+      const int at = c0 * kStep + (((i * 64 + lane) & ((1 << (cs + kUnits)) - 1)) << 4);
+      xv[i] = load16(a, at < kend * act_bytes(F) ? xo[i] : kOut, static_cast<uint32_t>(c0) * kStep);
     }
   }
   __device__ __forceinline__ void store_x(char* stage, int lane) {
@@ -403,16 +404,22 @@ template <Fmt F, int RT, int U, bool kAhead, bool kOrdered, int SLOTS, int STAGE
     cs = 0;   // log2 of a chunk's steps: as many as fit
     while (slots * ((kStep << (cs + 1)) + 16) <= STAGE - kStageZero && cs < 10) ++cs;
     if (s0 >= s1) return;
-    load_x(a, soff, s0, lane);
+    constexpr int kUnits = kStep == 64 ? 2 : 4;
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int unit = i * 64 + lane, slot = unit >> (cs + kUnits);
+      xo[i] = slot < slots ? soff(slot) + ((unit & ((1 << (cs + kUnits)) - 1)) << 4) : kOut;
+    }
+    load_x(a, s0, lane);
     w.load(wr, s0, kend, lane >> 4);
   }
 
   // acc[j][r] += rows of tile j times the 16 rows of W tile r; rslot[j]: slot of
   // the lane's row (lane % 16) of tile j (any, if the row is empty: its sums are
   // not read)
-  template <int NT, typename SlotOff>
-  __device__ __forceinline__ void run(floatx4 (&acc)[NT][RT], __amdgpu_buffer_rsrc_t a, SlotOff soff,
-                                      const int (&rslot)[NT], char* stage, int lane) {
+  template <int NT>
+  __device__ __forceinline__ void run(floatx4 (&acc)[NT][RT], __amdgpu_buffer_rsrc_t a, const int (&rslot)[NT],
+                                      char* stage, int lane) {
     if (s0 < s1) {
       const int q = lane >> 4, steps = 1 << cs;
       const char* zero = stage + STAGE - kStageZero;
@@ -432,18 +439,19 @@ template <Fmt F, int RT, int U, bool kAhead, bool kOrdered, int SLOTS, int STAGE
         for (int u = 0; u < U; ++u) {
           if ((u == 0 || kDense) && s + u >= cb + steps && s + u < s1) {
             cb = s + u;
-            load_x(a, soff, cb, lane);
+            load_x(a, cb, lane);
             store_x(stage, lane);
           }
           u32x4 x[NT][acts(F)];
 #pragma unroll
-          for (int j = 0; j < NT; ++j)
+          for (int j = 0; j < NT; ++j) {
+            const char* at = s + u < s1 ? xrow[j] + (s + u - cb) * kStep : zero;
 #pragma unroll
             for (int g = 0; g < acts(F); ++g) {
-              const char* at = xrow[j] + (s + u - cb) * kStep + mfma_k<F>(g) * act_bytes(F);
-              x[j][g] = *reinterpret_cast<const u32x4*>(s + u < s1 ? at : zero);
+              x[j][g] = *reinterpret_cast<const u32x4*>(at + mfma_k<F>(g) * act_bytes(F));
               if constexpr (is_w4(F) && !kOrdered) x[j][g] = to_code_order(x[j][g]);
             }
+          }
           multiply_step<F, NT, RT, U>(acc, kAhead ? ready : w, u, x, [&](int g) {
             return (s + u) * step_k(F) + (g << group_shift(F)) < kend ? 0xffffffffu : 0u;
           });

@@ -157,7 +157,7 @@ __global__ __launch_bounds__(NW * 64) void w4_linear_kernel(const uint16_t* x, W
   st.begin(rows_of<F, 1>(w, 0, n0, lane), xr, soff, M, s0, s1, w.K, lane);
   floatx4 acc[1][1] = {{floatx4{0.f, 0.f, 0.f, 0.f}}};
   const int rslot[1] = {min(lane & 15, M - 1)};
-  st.run(acc, xr, soff, rslot, mine, lane);
+  st.run(acc, xr, rslot, mine, lane);
   __syncthreads();
   *reinterpret_cast<floatx4*>(red + (wave * 64 + lane) * 4) = acc[0][0];
   __syncthreads();
