@@ -28,6 +28,7 @@ namespace {
 
 constexpr int kWaves = 8;                 // waves of a phase workgroup; they split k
 constexpr int kThreads = kWaves * kWave;
+constexpr int kParts = 4;                 // parts of the logits' sums, where there are several
 constexpr int kMaxT = MOE_MAX_DECODE_TOKENS;
 constexpr int kMaxE = MOE_MAX_EXPERTS + MOE_MAX_SHARED;
 
@@ -35,8 +36,8 @@ constexpr int kMaxE = MOE_MAX_EXPERTS + MOE_MAX_SHARED;
 // What the logits kernels leave besides the logits: zeroed counters for phase 2
 // and, for 4-bit weights, x in the order of the codes.
 __device__ __forceinline__ void prepare_phases(const DecodeArgs& a) {
-  const int nth = gridDim.x * gridDim.y * blockDim.x;
-  const int id = (blockIdx.y * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x;
+  const int nth = gridDim.x * gridDim.y * gridDim.z * blockDim.x;
+  const int id = ((blockIdx.z * gridDim.y + blockIdx.y) * gridDim.x + blockIdx.x) * blockDim.x + threadIdx.x;
   for (int i = id; i < a.ncounter; i += nth) a.counters[i] = 0;
   if (a.fmt == kDecodeW4)
     for (int i = id; i < a.T * (a.d / 8); i += nth)
@@ -111,8 +112,9 @@ __global__ __launch_bounds__(1024) void decode_logits_kernel(DecodeArgs a) {
 }
 
 // bf16, more tokens: 16 experts x 16 tokens per workgroup on the matrix cores,
-// 16 waves splitting d.  The float32 sums run over at most 256 elements and are
-// added in float64.
+// 16 waves and DecodeArgs::parts workgroups splitting d.  The float32 sums run over
+// at most 256 elements and are added in float64.  One part would leave most CUs
+// idle: 256 experts, d = 7168, 64 tokens 17 us, in four parts 8.
 __global__ __launch_bounds__(1024) void decode_logits_mfma_kernel(DecodeArgs a) {
   __shared__ double red[16][64][4];
   const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16;
@@ -124,7 +126,8 @@ __global__ __launch_bounds__(1024) void decode_logits_mfma_kernel(DecodeArgs a) 
   const uint32_t xo = t0 + r < a.T ? static_cast<uint32_t>(t0 + r) * pitch + 16u * q : kOut;
   const uint32_t go = e0 + r < a.E ? static_cast<uint32_t>(e0 + r) * pitch + 16u * q : kOut;
   const int nst = (a.d + 31) / 32;
-  const int s0 = wave * nst / 16, s1 = (wave + 1) * nst / 16;
+  const int slice = blockIdx.z * 16 + wave, slices = a.parts * 16;
+  const int s0 = slice * nst / slices, s1 = (slice + 1) * nst / slices;
   double acc[4] = {0.0, 0.0, 0.0, 0.0};
   for (int sb = s0; sb < s1; sb += 8) {
     u32x4 x[8], g[8];
@@ -152,8 +155,8 @@ __global__ __launch_bounds__(1024) void decode_logits_mfma_kernel(DecodeArgs a) 
       double l = 0.0;
 #pragma unroll
       for (int w = 0; w < 16; ++w) l += red[w][ln][i];
-      if (a.b_g != nullptr) l += static_cast<double>(a.b_g[e]);
-      a.logits[static_cast<size_t>(t) * a.E + e] = l;
+      if (a.b_g != nullptr && blockIdx.z == 0) l += static_cast<double>(a.b_g[e]);
+      a.logits[(static_cast<size_t>(blockIdx.z) * a.T + t) * a.E + e] = l;
     }
   }
   prepare_phases(a);
@@ -219,6 +222,9 @@ __device__ __forceinline__ void select_token(const DecodeArgs& a, int t, int lan
   for (int i = 0; i < 4; ++i) {
     const int e = lane + 64 * i;
     val[i] = e < a.E ? a.logits[static_cast<size_t>(t) * a.E + e] : 0.0;
+    if (a.parts > 1 && e < a.E)
+#pragma unroll
+      for (int p = 1; p < kParts; ++p) val[i] += a.logits[(static_cast<size_t>(p) * a.T + t) * a.E + e];
     double kv = val[i];
     if (a.b_sel != nullptr && e < a.E) kv += static_cast<double>(a.b_sel[e]);
     key[i] = kv == kv ? kv : -INFINITY;
@@ -771,7 +777,7 @@ void launch_logits(const DecodeArgs& a, hipStream_t st) {
   const int threads = a.d >= 8192 ? 1024 : (a.d / 8 + 63) / 64 * 64;
   if (a.T == 1) decode_logits_kernel<BF16, 1><<<dim3(a.E, 1), threads, 0, st>>>(a);
   else if (a.T <= 4) decode_logits_kernel<BF16, 4><<<dim3(a.E, 1), threads, 0, st>>>(a);
-  else if (BF16) decode_logits_mfma_kernel<<<dim3((a.E + 15) / 16, (a.T + 15) / 16), 1024, 0, st>>>(a);
+  else if (BF16) decode_logits_mfma_kernel<<<dim3((a.E + 15) / 16, (a.T + 15) / 16, a.parts), 1024, 0, st>>>(a);
   else decode_logits_kernel<BF16, 16><<<dim3(a.E, (a.T + 15) / 16), threads, 0, st>>>(a);
 }
 
@@ -790,6 +796,7 @@ void launch_logits(const DecodeArgs& a, hipStream_t st) {
 //            tokens of the DeepSeek shape, 14 batches: 8 waves 597 us, 4 536, 2 502;
 //            4-bit, d = 1024, two batches: 8 waves leave six without work)
 //   dense    bf16: over 16 tokens, eight and more to an expert
+//   parts    parts of each logit's sum, added by the selection
 DecodePlan decode_plan(int T, int d, int h, int E, int k, int S, int fmt) {
   const double used = E * (1.0 - std::pow(1.0 - static_cast<double>(k) / E, T)) + S;
   const double elem = fmt == kDecodeF32 ? 4.0 : fmt == kDecodeBf16 ? 2.0 : 0.5;
@@ -809,7 +816,8 @@ DecodePlan decode_plan(int T, int d, int h, int E, int k, int S, int fmt) {
   int ks = kWaves;
   while (ks > 1 && ks > nb) ks >>= 1;
   while (ks > 1 && nb / ks < 4 && used * h / (16. * rt1 * (2 * kWaves / ks)) >= 2.0 * slots1) ks >>= 1;
-  return DecodePlan{sp, used * d * h * elem >= (2 << 20) * static_cast<double>(slots1) ? 1 : 0, ks, dense ? 1 : 0};
+  const int parts = fmt != kDecodeF32 && T > 4 && d >= 1024 ? kParts : 1;
+  return DecodePlan{sp, used * d * h * elem >= (2 << 20) * static_cast<double>(slots1) ? 1 : 0, ks, dense ? 1 : 0, parts};
 }
 
 hipError_t launch_decode(const DecodeArgs& a, hipStream_t st) {

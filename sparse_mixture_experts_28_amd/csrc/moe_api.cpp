@@ -328,7 +328,7 @@ DecodeLayout decode_layout(int32_t T, int32_t d, int32_t h, int32_t E, int32_t k
   L.plan = decode_plan(T, d, h, E, k, S, fmt);
   L.ncounter = 2 + (d + 15) / 16;   // items handed out in phase 1 and 2, arrivals per column tile
   size_t off = 0;
-  L.logits = off;   off += align_up(static_cast<size_t>(T) * E * 8);
+  L.logits = off;   off += align_up(static_cast<size_t>(L.plan.parts) * T * E * 8);
   L.xord = off;     off += align_up(fmt == kDecodeW4 ? static_cast<size_t>(T) * d * 2 : 0);
   L.hid = off;      off += align_up(static_cast<size_t>(T) * (k + S) * h * 4);
   L.part = off;     off += align_up(L.plan.split > 1 ? static_cast<size_t>(L.plan.split) * T * d * 4 : 0);
@@ -371,6 +371,7 @@ moe_status_t forward_decode(DecodeArgs a, const moe_launch_t* launch) {
   a.dynamic = L.plan.dynamic;
   a.ksplit = L.plan.ksplit;
   a.dense = L.plan.dense;
+  a.parts = L.plan.parts;
   (void)hipGetLastError();
   const hipError_t e = launch_decode(a, launch->stream);
   if (e != hipSuccess) {

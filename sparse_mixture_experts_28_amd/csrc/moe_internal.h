@@ -343,7 +343,7 @@ struct DecodeArgs {
   void* out;            // [T, d]
   int32_t* topk_idx;    // [T, k]
   float* topk_w;        // [T, k]
-  double* logits;       // [T, E]
+  double* logits;       // [parts, T, E]
   void* xord;           // 4-bit weights: [T, d] x in the order of the codes
   void* hid;            // [T, k+S] hidden rows times the routing weight: h float32, or h bf16 values and h remainders
   float* part;          // [split, T, d] float32 (split > 1)
@@ -355,10 +355,11 @@ struct DecodeArgs {
   int split;            // shares of phase 2's sum per tile of output columns
   int dynamic;          // items handed out by a counter
   int dense;            // experts have many tokens each
+  int parts;            // parts of the logits' sums
   int ksplit;           // waves that split k in phase 1 (a power of two)
 };
 struct DecodePlan {
-  int split, dynamic, ksplit, dense;
+  int split, dynamic, ksplit, dense, parts;
 };
 DecodePlan decode_plan(int T, int d, int h, int E, int k, int S, int fmt);
 hipError_t launch_decode(const DecodeArgs& a, hipStream_t st);
