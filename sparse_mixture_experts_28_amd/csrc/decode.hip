@@ -493,8 +493,11 @@ __device__ __forceinline__ void run_tiles(St& st, floatx4 (&acc)[NT][RT], __amdg
 // ------------------------------------------------------------------ phase 1 --
 // One item: a job and hidden units, 16 for each group of KS waves.  The job's
 // tokens are the activation rows, NT tiles of 16; a group's waves split k and add
-// their sums in LDS in wave order.  The next item's first loads are issued before this one's sums, biases,
-// activations and stores.
+// their sums in LDS in wave order.  The next item's first loads are issued before
+// this one's sums, biases, activations and stores.  Bound by memory: the Mixtral
+// shape with one token 43 us (235 MB, 5.5 TB/s), the DeepSeek shape with 32 745 us
+// (4.5 GB, 6.0 TB/s); 4-bit with several tokens by vector operations (64 tokens
+// of the DeepSeek shape: 520 us, 3.5 TB/s).
 template <Fmt F, int TMAX, bool DENSE>
 __global__ __launch_bounds__(kThreads, (2 * Shape<F, TMAX, DENSE>::kWgs1)) void decode_phase1_kernel(DecodeArgs a) {
   using Sh = Shape<F, TMAX, DENSE>;
@@ -616,7 +619,8 @@ __device__ __forceinline__ void write_out(const DecodeArgs& a, const Routing& r,
 // 16), so an expert with one token costs one MFMA, and its sums go to its tokens
 // only.  Each wave adds them to a table of its own in LDS, [T][16 RT]; the tables
 // are added in wave order at the end.  Loads run ahead as in phase 1: the next
-// job's before a job's sums, the next item's before an item's.
+// job's before a job's sums, the next item's before an item's.  Bound as phase 1:
+// 43 us, 783 us, and 4-bit 653 us.
 template <Fmt F, int TMAX, bool DENSE>
 __global__ __launch_bounds__(kThreads, (2 * Shape<F, TMAX, DENSE>::kWgs2)) void decode_phase2_kernel(DecodeArgs a) {
   using Sh = Shape<F, TMAX, DENSE>;

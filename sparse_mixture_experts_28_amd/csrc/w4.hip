@@ -96,7 +96,9 @@ __device__ __forceinline__ void quantize8(u32x4 raw, long long i, uint32_t* code
 }
 
 // Two runs of 8 elements a thread, both loaded first.  n8 is a multiple of the
-// lanes of a group, so a group is in or out as a whole.
+// lanes of a group, so a group is in or out as a whole.  Bound by memory and, with
+// zero points, its operations: 2048 x 7168 in groups of 128 10 us (37 MB, 3.8 TB/s);
+// 8 x 1001 x 4096 in groups of 32 with zero points 19 us (85 MB, 4.4 TB/s).
 template <int GSHIFT, bool ZERO>
 __global__ __launch_bounds__(256) void w4_quantize_kernel(const uint16_t* src, long long n8, uint32_t* codes,
                                                           uint16_t* scales, uint8_t* zeros) {
@@ -112,7 +114,8 @@ __global__ __launch_bounds__(256) void w4_quantize_kernel(const uint16_t* src, l
 }
 
 // -------------------------------------------------------------- dequantize --
-// s (q - z): 8 bits times at most 5, exact in float32, one rounding to bf16.
+// s (q - z): 8 bits times at most 5, exact in float32, one rounding to bf16.  Bound
+// by its writes: 148 MB read and written in 25 us (5.9 TB/s).
 __global__ __launch_bounds__(256) void w4_dequantize_kernel(const uint32_t* codes, const uint16_t* scales,
                                                             const uint8_t* zeros, long long n8, int gshift,
                                                             uint16_t* dst) {
@@ -135,7 +138,9 @@ __global__ __launch_bounds__(256) void w4_dequantize_kernel(const uint32_t* code
 
 // ------------------------------------------------------------------ Linear --
 // y[m, n] = sum_k x[m, k] w[n, k] + b[n] for up to 16 rows.  One workgroup per 16
-// columns; its waves split k and add their sums in LDS in wave order.
+// columns; its waves split k and add their sums in LDS in wave order.  One row, N
+// 4096, K 14336, groups of 128: 11 us a call (30 MB, 4.8 us at the memory's rate: a
+// launch, and a wave's 3 to 4 batches one load latency each).
 template <Fmt F, int U, int NW, int STAGE>
 __global__ __launch_bounds__(NW * 64) void w4_linear_kernel(const uint16_t* x, WMat w, const uint16_t* bias,
                                                             uint16_t* y, int M) {
