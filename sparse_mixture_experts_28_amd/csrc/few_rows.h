@@ -55,7 +55,7 @@ struct WRows {
   uint32_t pair, tile;
   __amdgpu_buffer_rsrc_t s, z;   // 4-bit: the rows' scales and zero points
   uint32_t srow, stile;          // 4-bit: first scale of the lane's row, scales of 16 rows
-  bool wide;                     // 4-bit: no word of a batch's scales (zero points) is cut by the array's end
+  int slack;                     // 4-bit: scales from the last row's first to the array's end
 };
 
 template <Fmt F, int RT>
@@ -78,7 +78,7 @@ __device__ __forceinline__ WRows rows_of(const WMat& m, long long mat, int n0, i
     o.s = make_rsrc(m.s + row0 * ng, static_cast<uint32_t>(rest) * 2u);
     o.z = o.s;
     if (has_zeros(F)) o.z = make_rsrc(m.z + row0 * ng, static_cast<uint32_t>(rest));
-    o.wide = m.whole || static_cast<long long>(16 * RT) * ng + 64 <= rest;
+    o.slack = m.whole ? 0x7fffffff : static_cast<int>(rest - static_cast<long long>(left - 1) * ng);
     o.srow = static_cast<uint32_t>(r) * ng;
     o.stile = 16u * ng;
   } else {
@@ -103,7 +103,7 @@ __device__ __forceinline__ WRows rows_of(const WMat& m, long long mat, int n0, i
     }
     o.s = o.z = o.w;
     o.srow = o.stile = 0;
-    o.wide = false;
+    o.slack = 0;
   }
   return o;
 }
@@ -182,8 +182,9 @@ template <Fmt F> constexpr int mfma_k(int i) {
 // with the batch's scales, two to a word, and zero points, four to a word, in
 // every lane of their row, by loads as wide as they come, at any 2-byte (zero
 // points: 1-byte) address (one 2-byte load per step cost 3 to 5 us of a 23 us
-// phase); one by one only where such a load could leave the array, in its last
-// rows.
+// phase).  One by one only where the array's end could cut a word of a row that
+// is there: in the last batch of the last rows, where K / group is no multiple of
+// four.
 template <Fmt F, int RT, int U> struct WBatch {
   static constexpr int kS = is_w4(F) ? U << (7 - group_shift(F)) : 2;   // scales of a row and batch
   static_assert(kS >= 2 && kS <= 16, "whole words of scales");
@@ -226,7 +227,7 @@ template <Fmt F, int RT, int U> struct WBatch {
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         const uint32_t gi = wr.srow + r * wr.stile + g0;
-        if (wr.wide) {
+        if (static_cast<int>(g0) + kS <= wr.slack) {
           words(sc[r], wr.s, gi * 2u);
           if constexpr (has_zeros(F)) {
             if constexpr (kS == 2) zc[r][0] = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(wr.z, static_cast<int>(gi), 0, 0));
